@@ -80,6 +80,15 @@ typedef enum pa_q8_status {
 #define PA_Q8_DEV_BAD_BLOCK    0x1u  /* a block_tables entry >= num_blocks was skipped      */
 #define PA_Q8_DEV_BAD_SLOT     0x2u  /* a slot_mapping entry >= num_blocks*block_size (not PAD) */
 #define PA_Q8_DEV_WAIT_TIMEOUT 0x4u  /* a bounded in-kernel wait gave up; the output is void */
+#define PA_Q8_DEV_BAD_SEQ      0x8u  /* a request to the page pool named a row that does not exist
+                                        or cannot take it; the request was skipped */
+#define PA_Q8_DEV_NO_BLOCK    0x10u  /* the page pool ran out; the request was skipped */
+#define PA_Q8_DEV_BAD_ROWS    0x20u  /* query_starts falls or passes num_rows; the sequence was skipped */
+
+/* Element types of q and out where a call takes one. */
+#define PA_Q8_F32  0
+#define PA_Q8_F16  1
+#define PA_Q8_BF16 2
 
 /* Kernel families for pa_q8_decode_ex. */
 #define PA_Q8_KERNEL_AUTO 0
@@ -275,6 +284,124 @@ size_t pa_q8_decode_rows_workspace_size(int num_seqs, int num_rows, int num_head
                                         int max_blocks_per_seq, const pa_q8_decode_options *opts);
 
 /*
+ * pa_q8_prefill -- causal attention of prompt rows over the paged int8
+ * caches: packed sequences of different lengths, each a whole prompt or the
+ * next chunk of one whose earlier tokens the cache holds already (a cached or
+ * forked prefix).  The rows' own K and V are in the caches before the call
+ * (pa_q8_reshape_and_cache), as for pa_q8_decode_rows, whose result this is
+ * with a row count of its own for every sequence:
+ *
+ *   sequence s owns rows query_starts[s] .. query_starts[s + 1] - 1 of q and
+ *   out, n_s of them, the last n_s of its c = min(context_lens[s],
+ *   max_blocks_per_seq * block_size) tokens.  Its row i attends to the first
+ *   c - (n_s - 1 - i) tokens; a row that sees none is written as zeros.
+ *
+ *   out, q          device [num_rows][num_heads][head_size] of type dtype (PA_Q8_F32,
+ *                   PA_Q8_F16, PA_Q8_BF16), consecutive rows out_stride / q_stride
+ *                   elements apart (>= num_heads * head_size; q may be a column slice
+ *                   of fused QKV rows); pointers and strides multiples of 16 bytes;
+ *                   out must not overlap q
+ *   query_starts    device u32 [num_seqs + 1], rising; query_starts[0] may be > 0.  Rows
+ *                   of no sequence (before the first, behind the last) are left as
+ *                   they were.  A sequence whose bounds fall or pass num_rows is skipped
+ *                   and flagged PA_Q8_DEV_BAD_ROWS; one with no rows does nothing
+ *   num_rows        rows of q and out; 0 is a no-op
+ *   workspace       >= pa_q8_prefill_workspace_size() bytes, 16-byte aligned
+ * Every other argument is that of pa_q8_decode; block ids >= num_blocks are
+ * skipped and flagged.  The softmax runs in f32.  f32 rows keep 22 bits of q
+ * and of the weights through the tensor cores (two f16 parts each), f16 and
+ * bf16 rows 11 (one part).  num_heads / num_kv_heads up to 4096.
+ */
+int pa_q8_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64_t q_stride,
+                  const uint32_t *key_cache, const uint32_t *value_cache,
+                  const uint32_t *block_tables, const uint32_t *context_lens,
+                  const uint32_t *query_starts, int64_t num_rows, int num_seqs, int num_heads,
+                  int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq,
+                  int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+size_t pa_q8_prefill_workspace_size(int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads,
+                                    int head_size, int block_size, int max_blocks_per_seq, int dtype);
+
+/*
+ * ---- The pages of a cache ---------------------------------------------------
+ * A pool says who holds which page, on the device, so that a serving loop
+ * gives, shares and takes back pages without reading anything back:
+ *   ref_counts   u32 [num_blocks]: block_tables rows that hold the page
+ *   free_blocks  u32 [num_blocks]: a stack, the free pages in [0, *num_free)
+ *   num_free     u32 [1]
+ *   block_tables u32 [num_seqs][max_blocks_per_seq], context_lens u32 [num_seqs]:
+ *                the first ceil(context_lens[s] / block_size) entries of row s are held;
+ *                the entries behind them are neither read nor written
+ * One pool serves the caches of all layers, whose tables are the same; only
+ * pa_q8_copy_blocks touches a cache, and is called for each layer.  Calls on
+ * the same pool are ordered by their stream.  Requests are taken in the order
+ * of their index: the same calls give the same tables, counts and stack.  A
+ * request that cannot be met is skipped as a whole and flagged.
+ * num_blocks < 2^31; num_requests 0 is a no-op; workspace of >=
+ * pa_q8_pool_workspace_size() bytes, 16-byte aligned, contents irrelevant.
+ */
+size_t pa_q8_pool_workspace_size(int num_seqs, int64_t num_blocks, int num_requests);
+
+/* All pages free, page 0 on top; tables and lengths are the caller's to clear. */
+int pa_q8_pool_init(uint32_t *ref_counts, uint32_t *free_blocks, uint32_t *num_free,
+                    int64_t num_blocks, void *stream);
+
+/* Grow sequence seqs[i] to new_lens[i] tokens: pages are popped in request
+ * order and appended to its row, context_lens becomes new_lens[i].  A length
+ * not above the present one changes nothing.  Flagged and skipped: seqs[i] >=
+ * num_seqs, a row named by an earlier request, a length beyond the row
+ * (BAD_SEQ); a request that together with those before it needs more pages
+ * than are free (NO_BLOCK). */
+int pa_q8_extend_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts,
+                      uint32_t *free_blocks, uint32_t *num_free, const uint32_t *seqs,
+                      const uint32_t *new_lens, int num_requests, int num_seqs,
+                      int max_blocks_per_seq, int block_size, int64_t num_blocks,
+                      void *workspace, size_t workspace_bytes, void *stream);
+
+/* Make the empty row children[i] a copy of sequence parents[i] as it was
+ * before the call: whole pages are shared, a part-full last page becomes a
+ * fresh one.  copy_src[i], copy_dst[i] (u32 [num_requests]) name the page to
+ * copy, or 0xFFFFFFFF: pass them to pa_q8_copy_blocks for every layer before
+ * the child is read or extended.  Flagged and skipped: a row out of range, a
+ * child that is its own parent, is not empty or was named by an earlier
+ * request (BAD_SEQ); no free page (NO_BLOCK); a last page >= num_blocks
+ * (BAD_BLOCK). */
+int pa_q8_fork_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts,
+                    uint32_t *free_blocks, uint32_t *num_free, const uint32_t *parents,
+                    const uint32_t *children, uint32_t *copy_src, uint32_t *copy_dst,
+                    int num_requests, int num_seqs, int max_blocks_per_seq, int block_size,
+                    int64_t num_blocks, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Empty the rows seqs[i]; pages that no row holds any more go onto the stack,
+ * lowest number first.  A row named twice is freed once.  A page whose count
+ * is 0 already is flagged BAD_BLOCK and stays as it is.  No workspace. */
+int pa_q8_free_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts,
+                    uint32_t *free_blocks, uint32_t *num_free, const uint32_t *seqs,
+                    int num_requests, int num_seqs, int max_blocks_per_seq, int block_size,
+                    int64_t num_blocks, void *stream);
+
+/* Close the pool up: with L pages held, the k-th held page >= L becomes the
+ * k-th free page < L in every table, so pages 0 .. L - 1 are the held ones.
+ * move_src, move_dst (u32 [num_moves]; num_moves >= num_blocks / 2) get the
+ * pairs to pass to pa_q8_copy_blocks for every layer, 0xFFFFFFFF behind them.
+ * The stack is rewritten (the lowest free page on top, 0xFFFFFFFF behind it). */
+int pa_q8_compact_blocks(uint32_t *block_tables, const uint32_t *context_lens, uint32_t *ref_counts,
+                         uint32_t *free_blocks, uint32_t *num_free, uint32_t *move_src,
+                         uint32_t *move_dst, int64_t num_moves, int num_seqs,
+                         int max_blocks_per_seq, int block_size, int64_t num_blocks,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Copy page src_blocks[i] to page dst_blocks[i] of both caches, i <
+ * num_pairs.  Pairs with a 0xFFFFFFFF are skipped, pairs with another id >=
+ * num_blocks are skipped and flagged PA_Q8_DEV_BAD_BLOCK.  Two pairs with one
+ * destination, or a destination that is another pair's source, are a caller
+ * error (unspecified contents of that page).  Caches 16-byte aligned. */
+int pa_q8_copy_blocks(uint32_t *key_cache, uint32_t *value_cache, const uint32_t *src_blocks,
+                      const uint32_t *dst_blocks, int64_t num_pairs, int num_kv_heads,
+                      int head_size, int block_size, int64_t num_blocks, void *stream);
+
+/*
  * ---- The f32 cache variant ------------------------------------------------
  * "paged_attn_q8.comp" (header comment) describes itself as the math of
  * "paged_attn.comp" over an int8 cache instead of an f32 one ("1 byte/elem
@@ -297,6 +424,11 @@ int pa_f32_reshape_and_cache(const float *key, const float *value,
                              int64_t key_stride, int64_t value_stride,
                              int num_kv_heads, int head_size, int block_size,
                              int64_t num_blocks, void *stream);
+
+/* pa_q8_copy_blocks over the f32 caches. */
+int pa_f32_copy_blocks(float *key_cache, float *value_cache, const uint32_t *src_blocks,
+                       const uint32_t *dst_blocks, int64_t num_pairs, int num_kv_heads,
+                       int head_size, int block_size, int64_t num_blocks, void *stream);
 
 /* pa_q8_decode over the f32 caches (16-byte aligned), output = softmax(scale
  * * q . K^T) . V per (seq, head) with the same GQA map, clamp, empty-context

@@ -23,6 +23,12 @@ PA_Q8_KERNEL_TCGEN05 = 3
 PA_Q8_DEV_BAD_BLOCK = 0x1
 PA_Q8_DEV_BAD_SLOT = 0x2
 PA_Q8_DEV_WAIT_TIMEOUT = 0x4
+PA_Q8_DEV_BAD_SEQ = 0x8
+PA_Q8_DEV_NO_BLOCK = 0x10
+PA_Q8_DEV_BAD_ROWS = 0x20
+PA_Q8_F32 = 0
+PA_Q8_F16 = 1
+PA_Q8_BF16 = 2
 
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +98,26 @@ def lib() -> ctypes.CDLL:
         L.pa_q8_decode_plan.argtypes = [i32] * 6 + [ctypes.POINTER(DecodeOptions),
                                                     ctypes.POINTER(i32), ctypes.POINTER(i32),
                                                     ctypes.POINTER(i32), ctypes.POINTER(i64)]
+        L.pa_q8_prefill.restype = i32
+        L.pa_q8_prefill.argtypes = [P, P, i32, i64, i64, P, P, P, P, P, i64, i32, i32, i32, i32, i32, i32, i64, f32,
+                                    P, sz, P]
+        L.pa_q8_prefill_workspace_size.restype = sz
+        L.pa_q8_prefill_workspace_size.argtypes = [i64] + [i32] * 7
+        for copy in (L.pa_q8_copy_blocks, L.pa_f32_copy_blocks):
+            copy.restype = i32
+            copy.argtypes = [P, P, P, P, i64, i32, i32, i32, i64, P]
+        L.pa_q8_pool_workspace_size.restype = sz
+        L.pa_q8_pool_workspace_size.argtypes = [i32, i64, i32]
+        L.pa_q8_pool_init.restype = i32
+        L.pa_q8_pool_init.argtypes = [P, P, P, i64, P]
+        L.pa_q8_extend_seqs.restype = i32
+        L.pa_q8_extend_seqs.argtypes = [P] * 7 + [i32] * 4 + [i64, P, sz, P]
+        L.pa_q8_fork_seqs.restype = i32
+        L.pa_q8_fork_seqs.argtypes = [P] * 9 + [i32] * 4 + [i64, P, sz, P]
+        L.pa_q8_free_seqs.restype = i32
+        L.pa_q8_free_seqs.argtypes = [P] * 6 + [i32] * 4 + [i64, P]
+        L.pa_q8_compact_blocks.restype = i32
+        L.pa_q8_compact_blocks.argtypes = [P] * 7 + [i64, i32, i32, i32, i64, P, sz, P]
         L.pa_q8_device_status.restype = i32
         L.pa_q8_device_status.argtypes = [ctypes.POINTER(u32), i32, P]
         L.pa_q8_selftest_wait_timeout.restype = i32
@@ -406,6 +432,217 @@ def pa_q8c_decode(out, q, key_cache, value_cache, context_lens, *, num_kv_heads:
         ws_ptr, ws_bytes, _stream(stream), _opts(0, partition_tokens))
     _check("pa_q8c_decode", rc)
     return out
+
+
+def _ptr(t, dtype, name, device, numel=None, shape=None):
+    """Address of a contiguous CUDA tensor of the given type (u32 lists may be
+    int32) on `device`, with the number of elements or the shape asked for."""
+    import torch
+    ok = t.dtype in (torch.uint32, torch.int32) if dtype is torch.uint32 else t.dtype == dtype
+    if not ok or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of dtype {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    return t.data_ptr()
+
+
+def _current(device):
+    """The library queues on the current device: the tensors must be there."""
+    import torch
+    if device.type != "cuda":
+        raise TypeError("tensors must be CUDA tensors")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _scratch(need, workspace, device, stream):
+    """(address, bytes) of the caller's workspace, or of one allocated here and
+    kept from reuse until the work queued on `stream` is done with it."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if stream is not None:
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int)
+                                    else stream)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _row_type(dtype):
+    import torch
+    try:
+        return {torch.float32: PA_Q8_F32, torch.float16: PA_Q8_F16, torch.bfloat16: PA_Q8_BF16}[dtype]
+    except KeyError:
+        raise TypeError(f"q and out must be float32, float16 or bfloat16, got {dtype}") from None
+
+
+def pa_q8_prefill_workspace_size(num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                                 max_blocks_per_seq, dtype) -> int:
+    """Workspace bytes of pa_q8_prefill; dtype: the torch dtype of q."""
+    return int(lib().pa_q8_prefill_workspace_size(int(num_rows), int(num_seqs), int(num_heads), int(num_kv_heads),
+                                                  int(head_size), int(block_size), int(max_blocks_per_seq),
+                                                  _row_type(dtype)))
+
+
+def pa_q8_prefill(out, q, key_cache, value_cache, block_tables, context_lens, query_starts, *,
+                  num_kv_heads: int, block_size: int, scale: float, num_blocks: int | None = None,
+                  workspace=None, stream=None):
+    """out[T, H, D] = causal attention of packed prompt rows over the int8
+    pages (see include/pa_q8.h): rows query_starts[s] .. query_starts[s + 1] - 1
+    are the last ones of sequence s's context_lens[s] cached tokens.
+
+    q, out: float32, float16 or bfloat16 (the same), rows may be further apart
+    than H * D.  query_starts: u32 [S + 1].  Returns `out`.
+    """
+    import torch
+    T, H, D = q.shape
+    dt = _row_type(q.dtype)
+    dev = q.device
+    _current(dev)
+    if out.dtype != q.dtype or out.shape != q.shape or out.device != dev:
+        raise ValueError("out must be a tensor like q")
+    for t, name in ((q, "q"), (out, "out")):
+        if T and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+            raise ValueError(f"each row of {name} must be contiguous [num_heads, head_size]")
+    qs, os_ = (q.stride(0), out.stride(0)) if T > 1 else (H * D, H * D)
+    S, Nb = block_tables.shape
+    nb = int(key_cache.shape[0]) if num_blocks is None else int(num_blocks)
+    u32 = torch.uint32
+    args = (_ptr(key_cache, u32, "key_cache", dev), _ptr(value_cache, u32, "value_cache", dev),
+            _ptr(block_tables, u32, "block_tables", dev), _ptr(context_lens, u32, "context_lens", dev, S),
+            _ptr(query_starts, u32, "query_starts", dev, S + 1))
+    if value_cache.numel() != key_cache.numel() or nb * num_kv_heads * block_size * (D // 4 + 1) > key_cache.numel():
+        raise ValueError("the caches do not hold num_blocks pages of these sizes")
+    L = lib()
+    need = L.pa_q8_prefill_workspace_size(T, S, H, num_kv_heads, D, block_size, Nb, dt)
+    ws, ws_bytes = _scratch(need, workspace, dev, stream)
+    _check("pa_q8_prefill", L.pa_q8_prefill(
+        out.data_ptr(), q.data_ptr(), dt, os_, qs, *args, T, S, H, num_kv_heads, D, block_size, Nb, nb, scale,
+        ws, ws_bytes, _stream(stream)))
+    return out
+
+
+def _copy_blocks(fn, key_cache, value_cache, src_blocks, dst_blocks, dtype, head_size, num_blocks, stream):
+    import torch
+    dev = key_cache.device
+    _current(dev)
+    if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
+        raise ValueError("key_cache and value_cache must have one shape [num_blocks, num_kv_heads, block_size, ...]")
+    nb, hk, bs, _ = key_cache.shape
+    if num_blocks is not None:
+        if num_blocks > nb:
+            raise ValueError("the caches do not hold num_blocks pages")
+        nb = int(num_blocks)
+    n = src_blocks.numel()
+    _check(fn, getattr(lib(), fn)(
+        _ptr(key_cache, dtype, "key_cache", dev), _ptr(value_cache, dtype, "value_cache", dev),
+        _ptr(src_blocks, torch.uint32, "src_blocks", dev), _ptr(dst_blocks, torch.uint32, "dst_blocks", dev, n),
+        n, hk, head_size, bs, nb, _stream(stream)))
+
+
+def pa_q8_copy_blocks(key_cache, value_cache, src_blocks, dst_blocks, *, num_blocks: int | None = None,
+                      stream=None) -> None:
+    """Copy page src_blocks[i] to dst_blocks[i] of both q8 caches (0xFFFFFFFF: no pair)."""
+    import torch
+    _copy_blocks("pa_q8_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, torch.uint32,
+                 4 * (key_cache.shape[-1] - 1), num_blocks, stream)
+
+
+def pa_f32_copy_blocks(key_cache, value_cache, src_blocks, dst_blocks, *, num_blocks: int | None = None,
+                       stream=None) -> None:
+    """pa_q8_copy_blocks over the f32 caches [num_blocks, Hk, B, D]."""
+    import torch
+    _copy_blocks("pa_f32_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, torch.float32,
+                 key_cache.shape[-1], num_blocks, stream)
+
+
+def pa_q8_pool_workspace_size(num_seqs: int, num_blocks: int, num_requests: int = 0) -> int:
+    return int(lib().pa_q8_pool_workspace_size(int(num_seqs), int(num_blocks), int(num_requests)))
+
+
+def _pool(block_tables, context_lens, ref_counts, free_blocks, num_free):
+    """(device, rows, row length, pages, addresses) of a pool's tensors."""
+    import torch
+    dev = block_tables.device
+    _current(dev)
+    S, Nb = block_tables.shape
+    nb = ref_counts.numel()
+    u32 = torch.uint32
+    return dev, S, Nb, nb, (
+        _ptr(block_tables, u32, "block_tables", dev), _ptr(context_lens, u32, "context_lens", dev, S),
+        _ptr(ref_counts, u32, "ref_counts", dev), _ptr(free_blocks, u32, "free_blocks", dev, nb),
+        _ptr(num_free, u32, "num_free", dev, 1))
+
+
+def pa_q8_pool_init(ref_counts, free_blocks, num_free, *, stream=None) -> None:
+    """All pages of the pool free (see include/pa_q8.h)."""
+    import torch
+    dev, nb = ref_counts.device, ref_counts.numel()
+    _current(dev)
+    u32 = torch.uint32
+    _check("pa_q8_pool_init", lib().pa_q8_pool_init(
+        _ptr(ref_counts, u32, "ref_counts", dev), _ptr(free_blocks, u32, "free_blocks", dev, nb),
+        _ptr(num_free, u32, "num_free", dev, 1), nb, _stream(stream)))
+
+
+def pa_q8_extend_seqs(block_tables, context_lens, ref_counts, free_blocks, num_free, seqs, new_lens, *,
+                      block_size: int, workspace=None, stream=None) -> None:
+    """Grow sequence seqs[i] to new_lens[i] tokens, with pages from the pool."""
+    import torch
+    dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
+    n = seqs.numel()
+    L = lib()
+    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, dev, stream)
+    _check("pa_q8_extend_seqs", L.pa_q8_extend_seqs(
+        *pool, _ptr(seqs, torch.uint32, "seqs", dev), _ptr(new_lens, torch.uint32, "new_lens", dev, n), n, S, Nb,
+        block_size, nb, ws, ws_bytes, _stream(stream)))
+
+
+def pa_q8_fork_seqs(block_tables, context_lens, ref_counts, free_blocks, num_free, parents, children, copy_src,
+                    copy_dst, *, block_size: int, workspace=None, stream=None) -> None:
+    """Empty rows children[i] become copies of sequences parents[i]; the pages
+    to copy, for pa_q8_copy_blocks, go to copy_src / copy_dst."""
+    import torch
+    dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
+    n = parents.numel()
+    L = lib()
+    u32 = torch.uint32
+    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, dev, stream)
+    _check("pa_q8_fork_seqs", L.pa_q8_fork_seqs(
+        *pool, _ptr(parents, u32, "parents", dev), _ptr(children, u32, "children", dev, n),
+        _ptr(copy_src, u32, "copy_src", dev, n), _ptr(copy_dst, u32, "copy_dst", dev, n), n, S, Nb, block_size, nb,
+        ws, ws_bytes, _stream(stream)))
+
+
+def pa_q8_free_seqs(block_tables, context_lens, ref_counts, free_blocks, num_free, seqs, *, block_size: int,
+                    stream=None) -> None:
+    """Empty the rows seqs[i]; pages that no row holds go back to the pool."""
+    import torch
+    dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
+    _check("pa_q8_free_seqs", lib().pa_q8_free_seqs(
+        *pool, _ptr(seqs, torch.uint32, "seqs", dev), seqs.numel(), S, Nb, block_size, nb, _stream(stream)))
+
+
+def pa_q8_compact_blocks(block_tables, context_lens, ref_counts, free_blocks, num_free, move_src, move_dst, *,
+                         block_size: int, workspace=None, stream=None) -> None:
+    """Renumber the held pages to 0 .. L - 1; the moves, for pa_q8_copy_blocks,
+    go to move_src / move_dst (at least num_blocks // 2 entries)."""
+    import torch
+    dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
+    n = move_src.numel()
+    L = lib()
+    u32 = torch.uint32
+    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, 0), workspace, dev, stream)
+    _check("pa_q8_compact_blocks", L.pa_q8_compact_blocks(
+        *pool, _ptr(move_src, u32, "move_src", dev), _ptr(move_dst, u32, "move_dst", dev, n), n, S, Nb, block_size,
+        nb, ws, ws_bytes, _stream(stream)))
 
 
 def pa_q8_device_status(clear: bool = True, stream=None) -> int:

@@ -198,6 +198,83 @@ int cq_plan(pa_q8::DecodeArgs &a, const pa_q8_decode_options *opts, int sms) {
     return plan_for(a, &o, sms);
 }
 
+// Sizes and pointers of a call on the page pool (n: requests).
+int pool_check(const void *bt, const void *cl, const void *refs, const void *free_blocks, const void *num_free, int n,
+               int num_seqs, int max_blocks_per_seq, int block_size, int64_t num_blocks) {
+    if (n < 0 || num_seqs <= 0 || max_blocks_per_seq <= 0 || block_size <= 0 || num_blocks <= 0) return PA_Q8_EINVAL;
+    if (block_size % 4 != 0) return PA_Q8_EINVAL;
+    if (!pow2(block_size) || block_size > 1024 || num_blocks > 0x7FFFFFFF ||
+        (int64_t)max_blocks_per_seq * block_size > (int64_t)1 << 30)
+        return PA_Q8_EUNSUPPORTED;
+    if (!bt || !cl || !refs || !free_blocks || !num_free) return PA_Q8_EINVAL;
+    if (!aligned4(bt) || !aligned4(cl) || !aligned4(refs) || !aligned4(free_blocks) || !aligned4(num_free))
+        return PA_Q8_EALIGN;
+    return PA_Q8_OK;
+}
+
+// The two device lists of a call: both given, 4-byte aligned.
+int lists_check(const void *x, const void *y) {
+    if (!x || !y) return PA_Q8_EINVAL;
+    return aligned4(x) && aligned4(y) ? PA_Q8_OK : PA_Q8_EALIGN;
+}
+
+int pool_workspace_check(const void *workspace, size_t bytes, int num_seqs, int64_t num_blocks, int n) {
+    if (!workspace || bytes < pa_q8::pool_workspace_bytes(num_seqs, num_blocks, n)) return PA_Q8_EWORKSPACE;
+    return aligned16(workspace) ? PA_Q8_OK : PA_Q8_EALIGN;
+}
+
+int queued(cudaError_t e) {
+    if (e == cudaSuccess) return PA_Q8_OK;
+    cudaGetLastError();
+    return PA_Q8_ECUDA;
+}
+
+int copy_blocks_impl(uint32_t *key_cache, uint32_t *value_cache, const uint32_t *src, const uint32_t *dst,
+                     int64_t num_pairs, int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                     void *stream, int token_bytes) {
+    if (num_pairs < 0 || num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks <= 0) return PA_Q8_EINVAL;
+    if (head_size % 4 != 0 || block_size % 4 != 0) return PA_Q8_EINVAL;
+    if (!head_size_ok(head_size) || !pow2(block_size) || block_size > 1024) return PA_Q8_EUNSUPPORTED;
+    if (num_pairs > 0x7FFFFFFF || num_blocks > 0x7FFFFFFF) return PA_Q8_EUNSUPPORTED;
+    if (num_pairs == 0) return PA_Q8_OK;
+    if (!key_cache || !value_cache) return PA_Q8_EINVAL;
+    int rc = lists_check(src, dst);
+    if (rc != PA_Q8_OK) return rc;
+    if (!aligned16(key_cache) || !aligned16(value_cache)) return PA_Q8_EALIGN;
+    uint32_t *status = nullptr;
+    int sms = 0;
+    rc = device_info(&status, &sms);
+    if (rc != PA_Q8_OK) return rc;
+    return queued(pa_q8::launch_copy_pages(key_cache, value_cache, src, dst, num_pairs,
+                                           (int64_t)num_kv_heads * block_size * token_bytes, num_blocks, sms, status,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int dtype_bytes(int dtype) { return dtype == PA_Q8_F32 ? 4 : 2; }
+
+int check_prefill_shape(int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                        int block_size, int max_blocks_per_seq, int dtype) {
+    if (num_rows < 0 || dtype < PA_Q8_F32 || dtype > PA_Q8_BF16) return PA_Q8_EINVAL;
+    const int rc = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq);
+    if (rc != PA_Q8_OK) return rc;
+    if (num_rows > (int64_t)1 << 30 || num_heads / num_kv_heads > 4096) return PA_Q8_EUNSUPPORTED;
+    return PA_Q8_OK;
+}
+
+void prefill_fill(pa_q8::PrefillArgs &a, int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads,
+                  int head_size, int block_size, int max_blocks_per_seq, int dtype, int sms) {
+    std::memset(&a, 0, sizeof a);
+    a.dtype = dtype;
+    a.num_rows = num_rows;
+    a.num_seqs = num_seqs;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_size = head_size;
+    a.block_size = block_size;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_sms = sms;
+}
+
 }  // namespace
 
 extern "C" {
@@ -453,6 +530,156 @@ int pa_q8_decode(float *out, const float *q, const uint32_t *key_cache, const ui
     return pa_q8_decode_ex(out, q, key_cache, value_cache, block_tables, context_lens, num_seqs, num_heads,
                            num_kv_heads, head_size, block_size, max_blocks_per_seq, num_blocks, scale, workspace,
                            workspace_bytes, stream, nullptr);
+}
+
+size_t pa_q8_prefill_workspace_size(int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                                    int block_size, int max_blocks_per_seq, int dtype) {
+    if (check_prefill_shape(num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+                            dtype) != PA_Q8_OK)
+        return 0;
+    int sms = 0;
+    if (device_info(nullptr, &sms) != PA_Q8_OK) sms = 152;     // size query without a device
+    pa_q8::PrefillArgs a;
+    prefill_fill(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, dtype, sms);
+    return pa_q8::prefill_workspace_bytes(a);
+}
+
+int pa_q8_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64_t q_stride,
+                  const uint32_t *key_cache, const uint32_t *value_cache, const uint32_t *block_tables,
+                  const uint32_t *context_lens, const uint32_t *query_starts, int64_t num_rows, int num_seqs,
+                  int num_heads, int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq,
+                  int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = check_prefill_shape(num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                                 max_blocks_per_seq, dtype);
+    if (rc != PA_Q8_OK) return rc;
+    const int64_t row = (int64_t)num_heads * head_size;
+    if (num_blocks <= 0 || out_stride < row || q_stride < row) return PA_Q8_EINVAL;
+    if (num_rows == 0) return PA_Q8_OK;
+    if (!out || !q || !key_cache || !value_cache || !block_tables || !context_lens || !query_starts)
+        return PA_Q8_EINVAL;
+    const int vec = 16 / dtype_bytes(dtype);
+    if (!aligned16(out) || !aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) ||
+        !aligned4(block_tables) || !aligned4(context_lens) || !aligned4(query_starts) || out_stride % vec ||
+        q_stride % vec)
+        return PA_Q8_EALIGN;
+    uint32_t *status = nullptr;
+    int sms = 0;
+    rc = device_info(&status, &sms);
+    if (rc != PA_Q8_OK) return rc;
+    pa_q8::PrefillArgs a;
+    prefill_fill(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, dtype, sms);
+    const size_t need = pa_q8::prefill_workspace_bytes(a);
+    if (!workspace || workspace_bytes < need) return PA_Q8_EWORKSPACE;
+    if (!aligned16(workspace)) return PA_Q8_EALIGN;
+    a.out = out;
+    a.q = q;
+    a.out_stride = out_stride;
+    a.q_stride = q_stride;
+    a.key_cache = key_cache;
+    a.value_cache = value_cache;
+    a.block_tables = block_tables;
+    a.context_lens = context_lens;
+    a.query_starts = query_starts;
+    a.num_blocks = num_blocks;
+    a.scale = scale;
+    a.workspace = workspace;
+    a.status = status;
+    return queued(pa_q8::launch_prefill(a, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_q8_copy_blocks(uint32_t *key_cache, uint32_t *value_cache, const uint32_t *src_blocks,
+                      const uint32_t *dst_blocks, int64_t num_pairs, int num_kv_heads, int head_size, int block_size,
+                      int64_t num_blocks, void *stream) {
+    return copy_blocks_impl(key_cache, value_cache, src_blocks, dst_blocks, num_pairs, num_kv_heads, head_size,
+                            block_size, num_blocks, stream, head_size + 4);
+}
+
+int pa_f32_copy_blocks(float *key_cache, float *value_cache, const uint32_t *src_blocks, const uint32_t *dst_blocks,
+                       int64_t num_pairs, int num_kv_heads, int head_size, int block_size, int64_t num_blocks,
+                       void *stream) {
+    return copy_blocks_impl(reinterpret_cast<uint32_t *>(key_cache), reinterpret_cast<uint32_t *>(value_cache),
+                            src_blocks, dst_blocks, num_pairs, num_kv_heads, head_size, block_size, num_blocks, stream,
+                            4 * head_size);
+}
+
+size_t pa_q8_pool_workspace_size(int num_seqs, int64_t num_blocks, int num_requests) {
+    if (num_seqs <= 0 || num_blocks <= 0 || num_blocks > 0x7FFFFFFF || num_requests < 0) return 0;
+    return pa_q8::pool_workspace_bytes(num_seqs, num_blocks, num_requests);
+}
+
+int pa_q8_pool_init(uint32_t *ref_counts, uint32_t *free_blocks, uint32_t *num_free, int64_t num_blocks,
+                    void *stream) {
+    if (num_blocks <= 0 || !ref_counts || !free_blocks || !num_free) return PA_Q8_EINVAL;
+    if (num_blocks > 0x7FFFFFFF) return PA_Q8_EUNSUPPORTED;
+    if (!aligned4(ref_counts) || !aligned4(free_blocks) || !aligned4(num_free)) return PA_Q8_EALIGN;
+    const pa_q8::PoolArgs a{nullptr, nullptr, ref_counts, free_blocks, num_free, 0, 0, 0, num_blocks, nullptr};
+    return queued(pa_q8::launch_pool_init(a, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_q8_extend_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts, uint32_t *free_blocks,
+                      uint32_t *num_free, const uint32_t *seqs, const uint32_t *new_lens, int num_requests,
+                      int num_seqs, int max_blocks_per_seq, int block_size, int64_t num_blocks, void *workspace,
+                      size_t workspace_bytes, void *stream) {
+    int rc = pool_check(block_tables, context_lens, ref_counts, free_blocks, num_free, num_requests, num_seqs,
+                        max_blocks_per_seq, block_size, num_blocks);
+    if (rc != PA_Q8_OK || num_requests == 0) return rc;
+    if ((rc = lists_check(seqs, new_lens)) != PA_Q8_OK) return rc;
+    if ((rc = pool_workspace_check(workspace, workspace_bytes, num_seqs, num_blocks, num_requests)) != PA_Q8_OK) return rc;
+    uint32_t *status = nullptr;
+    if ((rc = device_info(&status, nullptr)) != PA_Q8_OK) return rc;
+    const pa_q8::PoolArgs a{block_tables, context_lens, ref_counts, free_blocks, num_free, num_seqs,
+                            max_blocks_per_seq, (uint32_t)block_size, num_blocks, status};
+    return queued(pa_q8::launch_extend(a, seqs, new_lens, num_requests, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_q8_fork_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts, uint32_t *free_blocks,
+                    uint32_t *num_free, const uint32_t *parents, const uint32_t *children, uint32_t *copy_src,
+                    uint32_t *copy_dst, int num_requests, int num_seqs, int max_blocks_per_seq, int block_size,
+                    int64_t num_blocks, void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = pool_check(block_tables, context_lens, ref_counts, free_blocks, num_free, num_requests, num_seqs,
+                        max_blocks_per_seq, block_size, num_blocks);
+    if (rc != PA_Q8_OK || num_requests == 0) return rc;
+    if ((rc = lists_check(parents, children)) != PA_Q8_OK) return rc;
+    if ((rc = lists_check(copy_src, copy_dst)) != PA_Q8_OK) return rc;
+    if ((rc = pool_workspace_check(workspace, workspace_bytes, num_seqs, num_blocks, num_requests)) != PA_Q8_OK) return rc;
+    uint32_t *status = nullptr;
+    if ((rc = device_info(&status, nullptr)) != PA_Q8_OK) return rc;
+    const pa_q8::PoolArgs a{block_tables, context_lens, ref_counts, free_blocks, num_free, num_seqs,
+                            max_blocks_per_seq, (uint32_t)block_size, num_blocks, status};
+    return queued(pa_q8::launch_fork(a, parents, children, num_requests, copy_src, copy_dst, workspace,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int pa_q8_free_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts, uint32_t *free_blocks,
+                    uint32_t *num_free, const uint32_t *seqs, int num_requests, int num_seqs, int max_blocks_per_seq,
+                    int block_size, int64_t num_blocks, void *stream) {
+    int rc = pool_check(block_tables, context_lens, ref_counts, free_blocks, num_free, num_requests, num_seqs,
+                        max_blocks_per_seq, block_size, num_blocks);
+    if (rc != PA_Q8_OK || num_requests == 0) return rc;
+    if ((rc = lists_check(seqs, seqs)) != PA_Q8_OK) return rc;
+    uint32_t *status = nullptr;
+    if ((rc = device_info(&status, nullptr)) != PA_Q8_OK) return rc;
+    const pa_q8::PoolArgs a{block_tables, context_lens, ref_counts, free_blocks, num_free, num_seqs,
+                            max_blocks_per_seq, (uint32_t)block_size, num_blocks, status};
+    return queued(pa_q8::launch_free(a, seqs, num_requests, static_cast<cudaStream_t>(stream)));
+}
+
+int pa_q8_compact_blocks(uint32_t *block_tables, const uint32_t *context_lens, uint32_t *ref_counts,
+                         uint32_t *free_blocks, uint32_t *num_free, uint32_t *move_src, uint32_t *move_dst,
+                         int64_t num_moves, int num_seqs, int max_blocks_per_seq, int block_size, int64_t num_blocks,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+    int rc = pool_check(block_tables, context_lens, ref_counts, free_blocks, num_free, 0, num_seqs,
+                        max_blocks_per_seq, block_size, num_blocks);
+    if (rc != PA_Q8_OK) return rc;
+    if (num_moves < num_blocks / 2) return PA_Q8_EINVAL;
+    if (num_moves > 0x7FFFFFFF) return PA_Q8_EUNSUPPORTED;
+    if (num_moves > 0 && (rc = lists_check(move_src, move_dst)) != PA_Q8_OK) return rc;
+    if ((rc = pool_workspace_check(workspace, workspace_bytes, num_seqs, num_blocks, 0)) != PA_Q8_OK) return rc;
+    uint32_t *status = nullptr;
+    if ((rc = device_info(&status, nullptr)) != PA_Q8_OK) return rc;
+    const pa_q8::PoolArgs a{block_tables, const_cast<uint32_t *>(context_lens), ref_counts, free_blocks, num_free,
+                            num_seqs, max_blocks_per_seq, (uint32_t)block_size, num_blocks, status};
+    return queued(pa_q8::launch_compact(a, move_src, move_dst, num_moves, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int pa_q8_device_status(uint32_t *bits, int clear, void *stream) {

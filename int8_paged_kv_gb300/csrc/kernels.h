@@ -106,6 +106,62 @@ int64_t plan_num_ctas(const DecodeArgs &a);
 
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t stream);
 
+// Causal attention of ragged prompt rows over the paged q8 caches.
+struct PrefillArgs {
+    void *out;
+    const void *q;
+    int dtype;             // PA_Q8_F32 / PA_Q8_F16 / PA_Q8_BF16
+    int64_t out_stride;    // elements between consecutive rows
+    int64_t q_stride;
+    const uint32_t *key_cache;
+    const uint32_t *value_cache;
+    const uint32_t *block_tables;
+    const uint32_t *context_lens;
+    const uint32_t *query_starts;
+    int64_t num_rows;
+    int num_seqs;
+    int num_heads;
+    int num_kv_heads;
+    int head_size;
+    int block_size;
+    int max_blocks_per_seq;
+    int64_t num_blocks;
+    float scale;
+    int num_sms;
+    void *workspace;
+    uint32_t *status;
+};
+
+size_t prefill_workspace_bytes(const PrefillArgs &a);
+cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
+
+// Page copies of a cache, and the pool of its pages (pages.cu).
+struct PoolArgs {
+    uint32_t *block_tables;   // [num_seqs][max_blocks_per_seq]
+    uint32_t *context_lens;   // [num_seqs]
+    uint32_t *ref_counts;     // [num_blocks]
+    uint32_t *free_blocks;    // [num_blocks], a stack: entries [0, *num_free)
+    uint32_t *num_free;
+    int num_seqs;
+    int max_blocks_per_seq;
+    uint32_t block_size;
+    int64_t num_blocks;
+    uint32_t *status;
+};
+
+cudaError_t launch_copy_pages(uint32_t *key, uint32_t *value, const uint32_t *src, const uint32_t *dst, int64_t pairs,
+                              int64_t page_bytes, int64_t num_blocks, int num_sms, uint32_t *status,
+                              cudaStream_t stream);
+size_t pool_workspace_bytes(int num_seqs, int64_t num_blocks, int num_requests);
+cudaError_t launch_pool_init(const PoolArgs &a, cudaStream_t stream);
+cudaError_t launch_fork(const PoolArgs &a, const uint32_t *parents, const uint32_t *children, int n, uint32_t *copy_src,
+                        uint32_t *copy_dst, void *workspace, cudaStream_t stream);
+cudaError_t launch_extend(const PoolArgs &a, const uint32_t *seqs, const uint32_t *new_lens, int n, void *workspace,
+                          cudaStream_t stream);
+cudaError_t launch_free(const PoolArgs &a, const uint32_t *seqs, int n, cudaStream_t stream);
+cudaError_t launch_compact(const PoolArgs &a, uint32_t *move_src, uint32_t *move_dst, int64_t capacity,
+                           void *workspace, cudaStream_t stream);
+
 cudaError_t launch_wait_selftest(uint32_t timeout_us, uint32_t *status, cudaStream_t stream);
 
 }  // namespace pa_q8
