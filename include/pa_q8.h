@@ -303,8 +303,9 @@ size_t pa_q8_decode_rows_workspace_size(int num_seqs, int num_rows, int num_head
  *                   out must not overlap q
  *   query_starts    device u32 [num_seqs + 1], rising; query_starts[0] may be > 0.  Rows
  *                   of no sequence (before the first, behind the last) are left as
- *                   they were.  A sequence whose bounds fall or pass num_rows is skipped
- *                   and flagged PA_Q8_DEV_BAD_ROWS; one with no rows does nothing
+ *                   they were.  A sequence that begins below an earlier start, ends below
+ *                   its own or ends behind num_rows is skipped and flagged
+ *                   PA_Q8_DEV_BAD_ROWS; one with no rows does nothing
  *   num_rows        rows of q and out; 0 is a no-op
  *   workspace       >= pa_q8_prefill_workspace_size() bytes, 16-byte aligned
  * Every other argument is that of pa_q8_decode; block ids >= num_blocks are

@@ -258,7 +258,17 @@ int check_prefill_shape(int64_t num_rows, int num_seqs, int num_heads, int num_k
     const int rc = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq);
     if (rc != PA_Q8_OK) return rc;
     if (num_rows > (int64_t)1 << 30 || num_heads / num_kv_heads > 4096) return PA_Q8_EUNSUPPORTED;
-    return PA_Q8_OK;
+    pa_q8::PrefillArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.dtype = dtype;
+    a.num_rows = num_rows;
+    a.num_seqs = num_seqs;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_size = head_size;
+    a.block_size = block_size;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    return pa_q8::prefill_ctas(a) > 0x7FFFFFFF ? PA_Q8_EUNSUPPORTED : PA_Q8_OK;   // grid x
 }
 
 void prefill_fill(pa_q8::PrefillArgs &a, int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads,

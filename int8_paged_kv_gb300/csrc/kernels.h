@@ -133,6 +133,7 @@ struct PrefillArgs {
 };
 
 size_t prefill_workspace_bytes(const PrefillArgs &a);
+int64_t prefill_ctas(const PrefillArgs &a);      // of the largest grid of a call
 cudaError_t launch_prefill(const PrefillArgs &a, cudaStream_t stream);
 
 // Page copies of a cache, and the pool of its pages (pages.cu).

@@ -285,10 +285,24 @@ def test_bad_pages_and_bad_bounds_are_flagged():
     got = c.run(bt=dev_u32(bt))
     assert device_status() == pk.PA_Q8_DEV_BAD_BLOCK
     assert torch.equal(got[:40], clean[:40]) and torch.equal(got[80:], clean[80:])
-    for bad in ([0, 40, 30, 120], [0, 40, 80, 121], [0, 40, 0xFFFFFFFF, 120]):
+    for bad in ([0, 40, 30, 120], [0, 40, 80, 121], [0, 40, 0xFFFFFFFF, 120], [0, 40, 0, 40]):
         got = c.run(qs=dev_u32(np.array(bad, dtype=np.uint32)))
         assert device_status() == pk.PA_Q8_DEV_BAD_ROWS
         assert torch.equal(got[:40], clean[:40])
+        assert bool(torch.isnan(got[80:]).all())
+
+
+@gpu
+def test_many_sequences_that_claim_the_same_rows():
+    """Bounds that swing up and down over 3000 sequences: only the first one's rows are its own."""
+    import torch
+    import int8_paged_kv_gb300 as pk
+    from tests.gpu_helpers import dev_u32, device_status
+    c = Case(8, 2, 64, 16, [64], [64], seed=21)
+    S = 3000
+    starts = dev_u32(np.array([0, 64] * (S // 2) + [0], dtype=np.uint32))
+    got = c.run(bt=c.bt.repeat(S, 1).contiguous(), cl=c.cl.repeat(S), qs=starts)
+    assert torch.equal(got, c.run()) and device_status() == pk.PA_Q8_DEV_BAD_ROWS
 
 
 @gpu
