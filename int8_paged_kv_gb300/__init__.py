@@ -26,5 +26,6 @@ _BINDING_NAMES = {
 def __getattr__(name):
     if name in _BINDING_NAMES:
         from . import _binding
-        return getattr(_binding, name)
+        value = globals()[name] = getattr(_binding, name)      # found without this function from now on
+        return value
     raise AttributeError(name)

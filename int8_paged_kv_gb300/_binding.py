@@ -47,6 +47,8 @@ class DecodeOptions(ctypes.Structure):
 def lib() -> ctypes.CDLL:
     """Load libpa_q8.so (built by int8_paged_kv_gb300.build); raise if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -434,44 +436,58 @@ def pa_q8c_decode(out, q, key_cache, value_cache, context_lens, *, num_kv_heads:
     return out
 
 
-def _ptr(t, dtype, name, device, numel=None, shape=None):
-    """Address of a contiguous CUDA tensor of the given type (u32 lists may be
-    int32) on `device`, with the number of elements or the shape asked for."""
-    import torch
-    ok = t.dtype in (torch.uint32, torch.int32) if dtype is torch.uint32 else t.dtype == dtype
-    if not ok or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor of dtype {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+def _address(t, dtypes, name, device, numel=-1):
+    """Address of a contiguous CUDA tensor of one of the given types on the
+    device with this index, with the number of elements asked for."""
+    if t.dtype not in dtypes or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of dtype {' or '.join(map(str, dtypes))}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
+    if numel >= 0 and t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     return t.data_ptr()
 
 
-def _current(device):
-    """The library queues on the current device: the tensors must be there."""
+def _u32():
     import torch
-    if device.type != "cuda":
+    return torch.int32, torch.uint32            # the same bits
+
+
+def _current(t):
+    """Index of the tensor's device, which has to be the current one: the
+    library queues there."""
+    import torch
+    if not t.is_cuda:
         raise TypeError("tensors must be CUDA tensors")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    device = t.get_device()
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return device
 
 
-def _scratch(need, workspace, device, stream):
+def _queue(stream, device):
+    """The stream's handle (None: the device's current stream)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _scratch(need, workspace, like, stream):
     """(address, bytes) of the caller's workspace, or of one allocated here and
-    kept from reuse until the work queued on `stream` is done with it."""
-    import torch
+    kept from reuse until the work queued on `stream` is done with it; `like`:
+    a tensor on the call's device."""
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        import torch
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
         if stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int)
+            workspace.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int)
                                     else stream)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace.data_ptr(), max(need, 16)
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
@@ -501,38 +517,34 @@ def pa_q8_prefill(out, q, key_cache, value_cache, block_tables, context_lens, qu
     q, out: float32, float16 or bfloat16 (the same), rows may be further apart
     than H * D.  query_starts: u32 [S + 1].  Returns `out`.
     """
-    import torch
     T, H, D = q.shape
     dt = _row_type(q.dtype)
-    dev = q.device
-    _current(dev)
-    if out.dtype != q.dtype or out.shape != q.shape or out.device != dev:
+    dev = _current(q)
+    if out.dtype != q.dtype or out.shape != q.shape or out.get_device() != dev:
         raise ValueError("out must be a tensor like q")
     for t, name in ((q, "q"), (out, "out")):
         if T and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
             raise ValueError(f"each row of {name} must be contiguous [num_heads, head_size]")
     qs, os_ = (q.stride(0), out.stride(0)) if T > 1 else (H * D, H * D)
     S, Nb = block_tables.shape
+    words = key_cache.numel()
     nb = int(key_cache.shape[0]) if num_blocks is None else int(num_blocks)
-    u32 = torch.uint32
-    args = (_ptr(key_cache, u32, "key_cache", dev), _ptr(value_cache, u32, "value_cache", dev),
-            _ptr(block_tables, u32, "block_tables", dev), _ptr(context_lens, u32, "context_lens", dev, S),
-            _ptr(query_starts, u32, "query_starts", dev, S + 1))
-    if value_cache.numel() != key_cache.numel() or nb * num_kv_heads * block_size * (D // 4 + 1) > key_cache.numel():
+    if nb * num_kv_heads * block_size * (D // 4 + 1) > words:
         raise ValueError("the caches do not hold num_blocks pages of these sizes")
+    u32 = _u32()
     L = lib()
     need = L.pa_q8_prefill_workspace_size(T, S, H, num_kv_heads, D, block_size, Nb, dt)
-    ws, ws_bytes = _scratch(need, workspace, dev, stream)
+    ws, ws_bytes = _scratch(need, workspace, q, stream)
     _check("pa_q8_prefill", L.pa_q8_prefill(
-        out.data_ptr(), q.data_ptr(), dt, os_, qs, *args, T, S, H, num_kv_heads, D, block_size, Nb, nb, scale,
-        ws, ws_bytes, _stream(stream)))
+        out.data_ptr(), q.data_ptr(), dt, os_, qs, _address(key_cache, u32, "key_cache", dev),
+        _address(value_cache, u32, "value_cache", dev, words), _address(block_tables, u32, "block_tables", dev),
+        _address(context_lens, u32, "context_lens", dev, S), _address(query_starts, u32, "query_starts", dev, S + 1),
+        T, S, H, num_kv_heads, D, block_size, Nb, nb, scale, ws, ws_bytes, _queue(stream, dev)))
     return out
 
 
-def _copy_blocks(fn, key_cache, value_cache, src_blocks, dst_blocks, dtype, head_size, num_blocks, stream):
-    import torch
-    dev = key_cache.device
-    _current(dev)
+def _copy_blocks(fn, key_cache, value_cache, src_blocks, dst_blocks, dtypes, head_size, num_blocks, stream):
+    dev = _current(key_cache)
     if key_cache.dim() != 4 or value_cache.shape != key_cache.shape:
         raise ValueError("key_cache and value_cache must have one shape [num_blocks, num_kv_heads, block_size, ...]")
     nb, hk, bs, _ = key_cache.shape
@@ -541,17 +553,17 @@ def _copy_blocks(fn, key_cache, value_cache, src_blocks, dst_blocks, dtype, head
             raise ValueError("the caches do not hold num_blocks pages")
         nb = int(num_blocks)
     n = src_blocks.numel()
+    u32 = _u32()
     _check(fn, getattr(lib(), fn)(
-        _ptr(key_cache, dtype, "key_cache", dev), _ptr(value_cache, dtype, "value_cache", dev),
-        _ptr(src_blocks, torch.uint32, "src_blocks", dev), _ptr(dst_blocks, torch.uint32, "dst_blocks", dev, n),
-        n, hk, head_size, bs, nb, _stream(stream)))
+        _address(key_cache, dtypes, "key_cache", dev), _address(value_cache, dtypes, "value_cache", dev),
+        _address(src_blocks, u32, "src_blocks", dev), _address(dst_blocks, u32, "dst_blocks", dev, n),
+        n, hk, head_size, bs, nb, _queue(stream, dev)))
 
 
 def pa_q8_copy_blocks(key_cache, value_cache, src_blocks, dst_blocks, *, num_blocks: int | None = None,
                       stream=None) -> None:
     """Copy page src_blocks[i] to dst_blocks[i] of both q8 caches (0xFFFFFFFF: no pair)."""
-    import torch
-    _copy_blocks("pa_q8_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, torch.uint32,
+    _copy_blocks("pa_q8_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, _u32(),
                  4 * (key_cache.shape[-1] - 1), num_blocks, stream)
 
 
@@ -559,7 +571,7 @@ def pa_f32_copy_blocks(key_cache, value_cache, src_blocks, dst_blocks, *, num_bl
                        stream=None) -> None:
     """pa_q8_copy_blocks over the f32 caches [num_blocks, Hk, B, D]."""
     import torch
-    _copy_blocks("pa_f32_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, torch.float32,
+    _copy_blocks("pa_f32_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, (torch.float32,),
                  key_cache.shape[-1], num_blocks, stream)
 
 
@@ -569,80 +581,73 @@ def pa_q8_pool_workspace_size(num_seqs: int, num_blocks: int, num_requests: int 
 
 def _pool(block_tables, context_lens, ref_counts, free_blocks, num_free):
     """(device, rows, row length, pages, addresses) of a pool's tensors."""
-    import torch
-    dev = block_tables.device
-    _current(dev)
+    dev = _current(block_tables)
     S, Nb = block_tables.shape
     nb = ref_counts.numel()
-    u32 = torch.uint32
+    u32 = _u32()
     return dev, S, Nb, nb, (
-        _ptr(block_tables, u32, "block_tables", dev), _ptr(context_lens, u32, "context_lens", dev, S),
-        _ptr(ref_counts, u32, "ref_counts", dev), _ptr(free_blocks, u32, "free_blocks", dev, nb),
-        _ptr(num_free, u32, "num_free", dev, 1))
+        _address(block_tables, u32, "block_tables", dev), _address(context_lens, u32, "context_lens", dev, S),
+        _address(ref_counts, u32, "ref_counts", dev), _address(free_blocks, u32, "free_blocks", dev, nb),
+        _address(num_free, u32, "num_free", dev, 1))
 
 
 def pa_q8_pool_init(ref_counts, free_blocks, num_free, *, stream=None) -> None:
     """All pages of the pool free (see include/pa_q8.h)."""
-    import torch
-    dev, nb = ref_counts.device, ref_counts.numel()
-    _current(dev)
-    u32 = torch.uint32
+    dev, nb = _current(ref_counts), ref_counts.numel()
+    u32 = _u32()
     _check("pa_q8_pool_init", lib().pa_q8_pool_init(
-        _ptr(ref_counts, u32, "ref_counts", dev), _ptr(free_blocks, u32, "free_blocks", dev, nb),
-        _ptr(num_free, u32, "num_free", dev, 1), nb, _stream(stream)))
+        _address(ref_counts, u32, "ref_counts", dev), _address(free_blocks, u32, "free_blocks", dev, nb),
+        _address(num_free, u32, "num_free", dev, 1), nb, _queue(stream, dev)))
 
 
 def pa_q8_extend_seqs(block_tables, context_lens, ref_counts, free_blocks, num_free, seqs, new_lens, *,
                       block_size: int, workspace=None, stream=None) -> None:
     """Grow sequence seqs[i] to new_lens[i] tokens, with pages from the pool."""
-    import torch
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     n = seqs.numel()
     L = lib()
-    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, dev, stream)
+    u32 = _u32()
+    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
     _check("pa_q8_extend_seqs", L.pa_q8_extend_seqs(
-        *pool, _ptr(seqs, torch.uint32, "seqs", dev), _ptr(new_lens, torch.uint32, "new_lens", dev, n), n, S, Nb,
-        block_size, nb, ws, ws_bytes, _stream(stream)))
+        *pool, _address(seqs, u32, "seqs", dev), _address(new_lens, u32, "new_lens", dev, n), n, S, Nb,
+        block_size, nb, ws, ws_bytes, _queue(stream, dev)))
 
 
 def pa_q8_fork_seqs(block_tables, context_lens, ref_counts, free_blocks, num_free, parents, children, copy_src,
                     copy_dst, *, block_size: int, workspace=None, stream=None) -> None:
     """Empty rows children[i] become copies of sequences parents[i]; the pages
     to copy, for pa_q8_copy_blocks, go to copy_src / copy_dst."""
-    import torch
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     n = parents.numel()
     L = lib()
-    u32 = torch.uint32
-    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, dev, stream)
+    u32 = _u32()
+    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
     _check("pa_q8_fork_seqs", L.pa_q8_fork_seqs(
-        *pool, _ptr(parents, u32, "parents", dev), _ptr(children, u32, "children", dev, n),
-        _ptr(copy_src, u32, "copy_src", dev, n), _ptr(copy_dst, u32, "copy_dst", dev, n), n, S, Nb, block_size, nb,
-        ws, ws_bytes, _stream(stream)))
+        *pool, _address(parents, u32, "parents", dev), _address(children, u32, "children", dev, n),
+        _address(copy_src, u32, "copy_src", dev, n), _address(copy_dst, u32, "copy_dst", dev, n), n, S, Nb,
+        block_size, nb, ws, ws_bytes, _queue(stream, dev)))
 
 
 def pa_q8_free_seqs(block_tables, context_lens, ref_counts, free_blocks, num_free, seqs, *, block_size: int,
                     stream=None) -> None:
     """Empty the rows seqs[i]; pages that no row holds go back to the pool."""
-    import torch
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     _check("pa_q8_free_seqs", lib().pa_q8_free_seqs(
-        *pool, _ptr(seqs, torch.uint32, "seqs", dev), seqs.numel(), S, Nb, block_size, nb, _stream(stream)))
+        *pool, _address(seqs, _u32(), "seqs", dev), seqs.numel(), S, Nb, block_size, nb, _queue(stream, dev)))
 
 
 def pa_q8_compact_blocks(block_tables, context_lens, ref_counts, free_blocks, num_free, move_src, move_dst, *,
                          block_size: int, workspace=None, stream=None) -> None:
     """Renumber the held pages to 0 .. L - 1; the moves, for pa_q8_copy_blocks,
     go to move_src / move_dst (at least num_blocks // 2 entries)."""
-    import torch
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     n = move_src.numel()
     L = lib()
-    u32 = torch.uint32
-    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, 0), workspace, dev, stream)
+    u32 = _u32()
+    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, 0), workspace, block_tables, stream)
     _check("pa_q8_compact_blocks", L.pa_q8_compact_blocks(
-        *pool, _ptr(move_src, u32, "move_src", dev), _ptr(move_dst, u32, "move_dst", dev, n), n, S, Nb, block_size,
-        nb, ws, ws_bytes, _stream(stream)))
+        *pool, _address(move_src, u32, "move_src", dev), _address(move_dst, u32, "move_dst", dev, n), n, S, Nb,
+        block_size, nb, ws, ws_bytes, _queue(stream, dev)))
 
 
 def pa_q8_device_status(clear: bool = True, stream=None) -> int:

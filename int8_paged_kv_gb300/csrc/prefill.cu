@@ -39,6 +39,7 @@ namespace {
 // Single: one row tile and one accumulator (head size 256 fills TMEM).
 enum Mode { kPair, kSplit, kSingle };
 
+// 64 tokens a job leave room in TMEM for the weights beside the logits.
 constexpr int kTN = 64;
 
 template <int D_, int NP_, Mode MODE_>
@@ -47,22 +48,24 @@ struct Cfg {
     static constexpr int NP = NP_;                        // f16 parts of q and of the weights
     static constexpr Mode MODE = MODE_;
     static constexpr int W = D / 4 + 1;                   // words per token vector
-    static constexpr int TN = kTN;                        // context tokens per K/V tile
+    static constexpr int TN = kTN;                        // context tokens per job
+    static constexpr int SUB = D == 256 ? 1 : 2;          // jobs' worth of tokens in a K/V tile: the conversion
+    static constexpr int CT = SUB * TN;                   // warps need that much at a time to hide their latencies
     static constexpr int NT = MODE == kPair ? 2 : 1;      // row tiles
     static constexpr int NS = MODE == kSingle ? 1 : 2;    // accumulators, softmax warpgroups
-    static constexpr int KST = D == 256 ? 2 : D == 64 ? 8 : 4;   // K tiles in shared memory
+    static constexpr int KST = D == 64 ? 4 : 2;           // K tiles in shared memory
     static constexpr int VST = D == 256 ? 3 - NP : KST;
-    static constexpr int DEPTH = KST < 4 ? 4 : KST;       // scale tables
+    static constexpr int DEPTH = 4;                       // scale tables
     static constexpr int CONV = 4;                        // conversion warps
     static constexpr int THREADS = 128 * (NS + 2);        // softmax, conversion, issue warpgroups
     static constexpr int ROWS = 128 * NT;
     static constexpr uint32_t Q_PART = 128u * D * 2;      // bytes of one f16 part of one row tile
-    static constexpr uint32_t KV_TILE = (uint32_t)TN * D * 2;
+    static constexpr uint32_t KV_TILE = (uint32_t)CT * D * 2;
     static constexpr uint32_t Q_OFF = 0;
     static constexpr uint32_t K_OFF = Q_OFF + NT * NP * Q_PART;
     static constexpr uint32_t V_OFF = K_OFF + KST * KV_TILE;
     static constexpr uint32_t TAB_OFF = V_OFF + VST * KV_TILE;
-    static constexpr uint32_t TAB = (2 * TN + 4) * 4;     // K scales, V scales, largest |V scale|
+    static constexpr uint32_t TAB = (2 * CT + 4) * 4;     // K scales, V scales, largest |V scale| of each job
     static constexpr uint32_t QF_OFF = TAB_OFF + DEPTH * TAB;
     static constexpr uint32_t X_OFF = QF_OFF + ROWS * 4;  // Split: R and sum of both accumulators
     static constexpr uint32_t BAR_OFF = X_OFF + (MODE == kSplit ? 2 * 2 * 128 * 4 : 0);
@@ -451,7 +454,7 @@ __device__ __forceinline__ void store8(T *p, const float *x) {
 // (commit of PV).
 template <typename T, typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
-    constexpr int D = C::D, TN = C::TN, NP = C::NP, NS = C::NS, W = C::W;
+    constexpr int D = C::D, TN = C::TN, CT = C::CT, SUB = C::SUB, NP = C::NP, NS = C::NS, W = C::W;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t s0 = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             const bool by_warps = i < C::KST || (i >= 2 * C::KST && i < 2 * C::KST + C::VST) ||
                                   (i >= B2 + 2 && i < B2 + 6);
             const bool table = i >= BT + C::DEPTH && i < B2;
-            mbar_init(bars + 8 * i, table ? 4 * C::NT : by_warps ? 4 : 1);
+            mbar_init(bars + 8 * i, table ? 4 * NS : by_warps ? 4 : 1);
         }
         *abort = 0u;
         fence_mbar_init();
@@ -498,8 +501,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     const uint32_t n = rows_of(a, e.x, row0), c = context_of(a, e.x);
     const int seen_all = most_seen(c, n, e.y * P.g.span, P.g.span);
     const int j0 = (int)e.z;
-    const int tiles = min((seen_all + TN - 1) / TN - j0, (int)P.plan.head[2]);
-    const int jobs = C::MODE == kPair ? 2 * tiles : tiles;
+    const int tiles = min((seen_all + CT - 1) / CT - j0, (int)P.plan.head[2]);
+    const int steps = min(tiles * SUB, (seen_all + TN - 1) / TN - j0 * SUB);     // of TN tokens
+    const int jobs = C::MODE == kPair ? 2 * steps : steps;
     const int head0 = slice * P.g.heads;                                 // first head of the kv head's group
     const int heads = min(P.g.heads, P.g.group - head0);
 
@@ -564,17 +568,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         // -------------------------------------------------- issue and tables
         set_regs_down<80>();
         // descriptors of the first tiles; offsets within and between tiles add to them in 16-byte units
-        auto tile_of = [](int job) { return C::MODE == kPair ? job >> 1 : job; };
+        auto step_of = [](int job) { return C::MODE == kPair ? job >> 1 : job; };
         if (warp == 4 * NS + 4 && elect_one()) {
             constexpr uint32_t ID_QK = umma_idesc_f16(128, TN);
             const uint64_t dQ = swizzled_desc(s0 + C::Q_OFF, 16), dK = swizzled_desc(s0 + C::K_OFF, 16);
             for (int job = 0; job < jobs; ++job) {
-                const int j = tile_of(job), st = j % C::KST, b = job & 1;
-                if ((C::MODE != kPair || b == 0) &&
-                    !wait_for(k_full(st), (j / C::KST) & 1, abort)) break;
+                const int step = step_of(job), j = step / SUB, st = j % C::KST, b = job & 1;
+                const bool first = step % SUB == 0 && (C::MODE != kPair || b == 0);
+                const bool last = step % SUB == SUB - 1 && (C::MODE != kPair || b == 1);
+                if (first && !wait_for(k_full(st), (j / C::KST) & 1, abort)) break;
                 if (job >= 2 && !wait_for(s_free(b), ((job >> 1) - 1) & 1, abort)) break;
                 tc_fence_after();
-                const uint64_t aK = dK + st * (C::KV_TILE / 16);
+                const uint64_t aK = dK + st * (C::KV_TILE / 16) + (step % SUB) * (TN * 128 / 16);
                 const uint64_t aQ = dQ + (C::MODE == kPair ? b : 0) * (NP * C::Q_PART / 16);
                 // the small parts first: what they add is not cut at the full sum's last bit
 #pragma unroll
@@ -582,21 +587,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
                         umma_f16(tmem + b * TN, aQ + (p * C::Q_PART + (k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
-                                 aK + ((k >> 2) * TN * 128 + (k & 3) * 32) / 16, ID_QK, p < NP - 1 || k > 0);
+                                 aK + ((k >> 2) * CT * 128 + (k & 3) * 32) / 16, ID_QK, p < NP - 1 || k > 0);
                 umma_commit(s_full(b));
-                if ((C::MODE != kPair || b == 1) && j + C::KST < tiles) umma_commit(k_free(st));
+                if (last && j + C::KST < tiles) umma_commit(k_free(st));
                 issued = true;
             }
         } else if (warp == 4 * NS + 5 && elect_one()) {
             constexpr uint32_t ID_PV = umma_idesc_f16(128, D) | 1u << 16;       // B is MN-major
-            const uint64_t dV = swizzled_desc(s0 + C::V_OFF, TN * 128);
+            const uint64_t dV = swizzled_desc(s0 + C::V_OFF, CT * 128);
             for (int job = 0; job < jobs; ++job) {
-                const int j = tile_of(job), st = j % C::VST, b = job & 1;
-                if ((C::MODE != kPair || b == 0) &&
-                    !wait_for(v_full(st), (j / C::VST) & 1, abort)) break;
+                const int step = step_of(job), j = step / SUB, st = j % C::VST, b = job & 1;
+                const bool first = step % SUB == 0 && (C::MODE != kPair || b == 0);
+                const bool last = step % SUB == SUB - 1 && (C::MODE != kPair || b == 1);
+                if (first && !wait_for(v_full(st), (j / C::VST) & 1, abort)) break;
                 if (!wait_for(p_full(b), (job >> 1) & 1, abort)) break;
                 tc_fence_after();
-                const uint64_t aV = dV + st * (C::KV_TILE / 16);
+                const uint64_t aV = dV + st * (C::KV_TILE / 16) + (step % SUB) * (TN * 128 / 16);
                 const uint32_t tP = tmem + C::TM_P + b * (NP * TN / 2);
                 const bool more = C::MODE == kSingle ? job > 0 : job > 1;
 #pragma unroll
@@ -606,25 +612,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                         umma_f16_ta(tO + (C::MODE == kSingle ? 0 : b * D), tP + p * (TN / 2) + 8 * k,
                                     aV + k * (2048 / 16), ID_PV, more || p < NP - 1 || k > 0);
                 umma_commit(pv_done(b));
-                if ((C::MODE != kPair || b == 1) && j + C::VST < tiles) umma_commit(v_free(st));
+                if (last && j + C::VST < tiles) umma_commit(v_free(st));
                 issued = true;
             }
         }
         __syncwarp();
         if (warp == 4 * NS + 6) {
-            // tokens lane and lane + 32 of a tile; the next tile's scales and the
-            // pages of the one after it are in flight
+            // tokens lane + 32 u of a tile; the next tile's scales and the pages of
+            // the one after it are in flight
+            constexpr int PER = CT / 32;
             const Pages pages(a, e.x, kvh, W, P.log2B);
-            float ks[2], vs[2];
-            uint32_t page[2];
-            auto token = [&](int j, int u) { return (j0 + j) * TN + 32 * u + lane; };
+            float ks[PER], vs[PER];
+            uint32_t page[PER];
+            auto token = [&](int j, int u) { return (j0 + j) * CT + 32 * u + lane; };
             auto find = [&](int j) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) page[u] = token(j, u) < seen_all ? pages.find(token(j, u)) : 0u;
+                for (int u = 0; u < PER; ++u) page[u] = token(j, u) < seen_all ? pages.find(token(j, u)) : 0u;
             };
             auto load = [&](int j) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < PER; ++u) {
                     ks[u] = vs[u] = 0.0f;                    // tokens no row sees, or on no page
                     if (token(j, u) >= seen_all) continue;
                     if (page[u] < a.num_blocks) {
@@ -645,16 +652,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                     !__all_sync(0xFFFFFFFFu, wait_for(t_free(tab), (j / C::DEPTH - 1) & 1, abort)))
                     break;
                 float *table = reinterpret_cast<float *>(smem + C::TAB_OFF + tab * C::TAB);
-                uint32_t top = 0;                            // the largest finite |V scale|
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    table[32 * u + lane] = ks[u] * P.scale_log2;
-                    table[TN + 32 * u + lane] = vs[u];
-                    const uint32_t bits = __float_as_uint(vs[u]) & 0x7FFFFFFFu;
-                    top = max(top, bits < 0x7F800000u ? bits : 0u);
+                for (int u = 0; u < PER; u += 2) {
+                    uint32_t top = 0;                        // the largest finite |V scale| of a job
+#pragma unroll
+                    for (int x = u; x < u + 2; ++x) {
+                        table[32 * x + lane] = ks[x] * P.scale_log2;
+                        table[CT + 32 * x + lane] = vs[x];
+                        const uint32_t bits = __float_as_uint(vs[x]) & 0x7FFFFFFFu;
+                        top = max(top, bits < 0x7F800000u ? bits : 0u);
+                    }
+                    top = __reduce_max_sync(0xFFFFFFFFu, top);
+                    if (lane == 0) table[2 * CT + u / 2] = __uint_as_float(top);
                 }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-                if (lane == 0) table[2 * TN] = __uint_as_float(top);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(t_full(tab));
                 load(j + 1);
@@ -665,7 +675,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         // ------------------------------------------------------- conversion
         if (NS == 2) set_regs_down<112>();
         const int cw = warp - 4 * NS;
-        constexpr int TPW = TN / C::CONV;                    // tokens of a tile per warp
+        constexpr int TPW = CT / C::CONV;                    // tokens of a tile per warp
         constexpr int NW = TPW * (W - 1) / 32;               // words of a tile per lane
         const Pages pages(a, e.x, kvh, W, P.log2B);
         const F16Consts fc;
@@ -673,7 +683,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         uint32_t page = 0;
         uint64_t off = 0;                                    // of this lane's token of the tile loaded last
         // this lane's token of tile j (lanes above TPW repeat the ones below)
-        auto token = [&](int j) { return (j0 + j) * TN + cw * TPW + (lane % TPW); };
+        auto token = [&](int j) { return (j0 + j) * CT + cw * TPW + (lane % TPW); };
         auto find = [&](int j) { page = token(j) < seen_all ? pages.find(token(j)) : 0u; };
         // The words of the warp's tokens, four tokens at a time: they are on one
         // page, W words apart.  Behind the last token that is seen, the other
@@ -703,7 +713,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             for (int i = 0; i < NW; ++i) {
                 uint2 v;
                 codes4_to_f16x2(w[i], v.x, v.y, fc);
-                *reinterpret_cast<uint2 *>(tile + swz(cw * TPW + token_at(i), 4 * word_at(i), TN)) = v;
+                *reinterpret_cast<uint2 *>(tile + swz(cw * TPW + token_at(i), 4 * word_at(i), CT)) = v;
             }
         };
         auto ready = [&](uint32_t bar) {
@@ -758,15 +768,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         float R = -INFINITY;
         float2 l2 = make_float2(0.0f, 0.0f);
         bool ok = true;
-        auto tile_job = [&](auto mask_c, int job, int j, int b) {
+        auto tile_job = [&](auto mask_c, int job, int step, int b) {
             constexpr bool MASK = decltype(mask_c)::value;
-            const float *table = reinterpret_cast<const float *>(smem + C::TAB_OFF + (j % C::DEPTH) * C::TAB);
+            const int tab = step / SUB % C::DEPTH, sub = step % SUB;
+            // this job's K scales; its V scales are CT further, the largest of them at `vtop`
+            const float *table = reinterpret_cast<const float *>(smem + C::TAB_OFF + tab * C::TAB) + sub * TN;
+            const float vtop = reinterpret_cast<const float *>(smem + C::TAB_OFF + tab * C::TAB)[2 * CT + sub];
             const uint32_t tS = tmem + b * TN + lanes;
             float z[TN];
 #pragma unroll
             for (int k = 0; k < TN; k += 32) tmem_ld32_nowait(tS + k, z + k);
-            float vmax = table[2 * TN];
-            const int rel = sees - (j0 + j) * TN;            // columns below it are seen
+            float vmax = vtop;
+            const int rel = sees - (j0 * SUB + step) * TN;   // columns below it are seen
             tmem_wait_ld();
 #pragma unroll
             for (int k = 0; k < TN; k += 32) behind32(z + k);
@@ -777,7 +790,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 vmax = 0.0f;
 #pragma unroll
                 for (int k = 0; k < TN; ++k) {
-                    const float v = fabsf(table[TN + k]);
+                    const float v = fabsf(table[CT + k]);
                     if (k < rel && v < INFINITY) vmax = fmaxf(vmax, v);
                 }
             }
@@ -843,7 +856,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
-                    const float4 v4 = *reinterpret_cast<const float4 *>(table + TN + k0 + k);
+                    const float4 v4 = *reinterpret_cast<const float4 *>(table + CT + k0 + k);
                     float2 x = fma_f2(make_float2(z[k0 + k], z[k0 + k + 1]), q2, r2);
                     float2 y = fma_f2(make_float2(z[k0 + k + 2], z[k0 + k + 3]), q2, r2);
                     x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
@@ -875,17 +888,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(p_full(b));
-                mbar_arrive(t_free(j % C::DEPTH));
+                // Split: each softmax warpgroup has one of a tile's two jobs
+                if (C::MODE == kSplit || sub == SUB - 1) mbar_arrive(t_free(tab));
             }
         };
         for (int job = C::MODE == kSingle ? 0 : wg; job < jobs; job += NS) {
-            const int j = C::MODE == kPair ? job >> 1 : job, b = job & 1;
+            const int step = C::MODE == kPair ? job >> 1 : job, j = step / SUB, b = job & 1;
             ok = wait_for(t_full(j % C::DEPTH), (j / C::DEPTH) & 1, abort) &&
                  wait_for(s_full(b), (job >> 1) & 1, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
-            if ((j0 + j + 1) * TN > sees_min) tile_job(std::true_type(), job, j, b);
-            else tile_job(std::false_type(), job, j, b);
+            if ((j0 * SUB + step + 1) * TN > sees_min) tile_job(std::true_type(), job, step, b);
+            else tile_job(std::false_type(), job, step, b);
             if (!ok) break;
         }
         // ---- the row's result: normalised, or as the piece's record
@@ -1049,7 +1063,7 @@ size_t layout(const PrefillArgs &a, Params &P) {
     g.span = nt * g.tokens;
     g.groups = a.num_kv_heads * g.slices;
     P.rows = 128 * nt;
-    P.tn = kTN;
+    P.tn = a.head_size == 256 ? kTN : 2 * kTN;           // tokens of a K/V tile: items are cut between tiles
     const int64_t least = (a.num_rows + g.span - 1) / g.span;        // items, at least and at most
     const int64_t most = a.num_rows / g.span + (a.num_seqs < a.num_rows ? a.num_seqs : a.num_rows);
     P.may_split = least * g.groups < 2 * kWave * 3 / 4 &&
