@@ -72,10 +72,15 @@ struct Cfg {
     static constexpr int BARS = 2 * KST + 2 * VST + 2 * DEPTH + 8 + 2;
     static constexpr uint32_t SMEM = BAR_OFF + BARS * 8 + 8;
     // TMEM columns: S twice, the weights' parts twice (two f16 a column), the accumulators
-    static constexpr int TM_P = 2 * TN, TM_O = TM_P + TN * NP;
+    static constexpr int TM_P = 2 * TN, TM_O = TM_P + TN * NP, TM_Q = TM_O + NS * D;
+    // ... and, in what is left, the first QT columns of 32 f16 pairs (64 head
+    // dimensions) of each Q tile and part: read from there by QK, they spare
+    // shared memory, whose bandwidth bounds the kernel
+    static constexpr int QT_ROOM = (512 - TM_Q) / (32 * NT * NP);
+    static constexpr int QT = QT_ROOM < D / 64 ? QT_ROOM : D / 64;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
     static_assert(SMEM > 232448 / 2, "one CTA per SM: each takes all of TMEM");
-    static_assert(TM_O + NS * D <= 512, "TMEM");
+    static_assert(TM_Q + NT * NP * QT * 32 <= 512, "TMEM");
 };
 
 // One CTA's work: rows of a tile of a sequence against K/V tiles [j0, j1).
@@ -562,6 +567,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
     const uint32_t tO = tmem + C::TM_O;
+    if constexpr (C::QT > 0) {
+        // the softmax warpgroups' threads carry a Q row each
+        if (warp < 4 * C::NT && tiles > 0) {
+            const int rt = tid & 127, nt = warp >> 2;
+#pragma unroll
+            for (int p = 0; p < NP; ++p)
+#pragma unroll
+                for (int q = 0; q < C::QT; ++q) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        *reinterpret_cast<uint4 *>(v + 4 * x) = *reinterpret_cast<const uint4 *>(
+                            smem + C::Q_OFF + (nt * NP + p) * C::Q_PART + swz(rt, 64 * q + 8 * x, 128));
+                    const uint32_t at = tmem + C::TM_Q + (nt * NP + p) * (32 * C::QT) + 32 * q +
+                                        ((uint32_t)(32 * (warp & 3)) << 16);
+                    tmem_st16_nowait(at, v);
+                    tmem_st16_nowait(at + 16, v + 16);
+                }
+            tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
     bool issued = false;
 
     if (warp >= 4 * NS + 4) {
@@ -586,7 +615,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        umma_f16(tmem + b * TN, aQ + (p * C::Q_PART + (k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
+                        if (k < 4 * C::QT)
+                            umma_f16_ta(tmem + b * TN,
+                                        tmem + C::TM_Q + ((C::MODE == kPair ? b : 0) * NP + p) * (32 * C::QT) + 8 * k,
+                                        aK + ((k >> 2) * CT * 128 + (k & 3) * 32) / 16, ID_QK, p < NP - 1 || k > 0);
+                        else umma_f16(tmem + b * TN, aQ + (p * C::Q_PART + (k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
                                  aK + ((k >> 2) * CT * 128 + (k & 3) * 32) / 16, ID_QK, p < NP - 1 || k > 0);
                 umma_commit(s_full(b));
                 if (last && j + C::KST < tiles) umma_commit(k_free(st));
@@ -696,11 +729,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         auto locate = [&](int j) {
             off = token(j) < seen_all && page < a.num_blocks ? pages.offset(page, token(j)) : 0;
         };
-        auto load = [&](const uint32_t *cache, uint32_t (&w)[NW]) {
+        auto load = [&](const uint32_t *cache, uint64_t at, uint32_t (&w)[NW]) {
             constexpr int PER4 = 4 * NW / TPW;               // words of four tokens per lane
 #pragma unroll
             for (int f = 0; f < TPW / 4; ++f) {
-                const uint64_t from = __shfl_sync(0xFFFFFFFFu, off, 4 * f) + 4 * word_at(0) +
+                const uint64_t from = __shfl_sync(0xFFFFFFFFu, at, 4 * f) + 4 * word_at(0) +
                                       4 * W * (D == 64 ? lane >> 4 : 0);
 #pragma unroll
                 for (int i = 0; i < PER4; ++i)
@@ -721,18 +754,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // K(0), then K(j + 1) ahead of V(j): logits do not wait for a V tile's place
+        // K(0), then K(j + 1) ahead of V(j): logits do not wait for a V tile's
+        // place.  A tile's words are asked for when the registers are free, one
+        // conversion (of the other cache) before they are used.
         find(0);
         locate(0);
-        load(a.key_cache, kw);
+        load(a.key_cache, off, kw);
         find(1);
         for (int j = 0; j <= tiles; ++j) {
+            const uint64_t off_v = off;                      // tile j's
             if (j < tiles) {
                 const int st = j % C::KST;
                 if (j >= C::KST &&
                     !__all_sync(0xFFFFFFFFu, wait_for(k_free(st), (j / C::KST - 1) & 1, abort)))
                     break;
                 convert(smem + C::K_OFF + st * C::KV_TILE, kw);
+                locate(j + 1);
+                load(a.key_cache, off, kw);                  // K(j + 1)
+                find(j + 2);
                 ready(k_full(st));
             }
             if (j > 0) {
@@ -743,11 +782,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 convert(smem + C::V_OFF + st * C::KV_TILE, vw);
                 ready(v_full(st));
             }
-            if (j == tiles) break;
-            load(a.value_cache, vw);                         // V(j): off is tile j's
-            locate(j + 1);
-            load(a.key_cache, kw);                           // K(j + 1)
-            find(j + 2);
+            if (j < tiles) load(a.value_cache, off_v, vw);   // V(j)
         }
     } else {
         // ---------------------------------------------------------- softmax
