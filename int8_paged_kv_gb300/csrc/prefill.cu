@@ -39,6 +39,10 @@ namespace {
 // Single: one row tile and one accumulator (head size 256 fills TMEM).
 enum Mode { kPair, kSplit, kSingle };
 
+// Jobs after which an accumulator of f32 rows is added to sums of its own (an
+// error of 1e-5 of what it holds has gathered by then, where all terms have one sign).
+constexpr int kFlush = 32;
+
 // 64 tokens a job leave room in TMEM for the weights beside the logits.
 constexpr int kTN = 64;
 
@@ -59,6 +63,7 @@ struct Cfg {
     static constexpr int CONV = 4;                        // conversion warps
     static constexpr int THREADS = 128 * (NS + 2);        // softmax, conversion, issue warpgroups
     static constexpr int ROWS = 128 * NT;
+    static constexpr int FLUSH = NP == 2 ? kFlush : 1 << 29;   // 16-bit rows: never
     static constexpr uint32_t Q_PART = 128u * D * 2;      // bytes of one f16 part of one row tile
     static constexpr uint32_t KV_TILE = (uint32_t)CT * D * 2;
     static constexpr uint32_t Q_OFF = 0;
@@ -67,10 +72,10 @@ struct Cfg {
     static constexpr uint32_t TAB_OFF = V_OFF + VST * KV_TILE;
     static constexpr uint32_t TAB = (2 * CT + 4) * 4;     // K scales, V scales, largest |V scale| of each job
     static constexpr uint32_t QF_OFF = TAB_OFF + DEPTH * TAB;
-    static constexpr uint32_t X_OFF = QF_OFF + ROWS * 4;  // Split: R and sum of both accumulators
-    static constexpr uint32_t BAR_OFF = X_OFF + (MODE == kSplit ? 2 * 2 * 128 * 4 : 0);
+    static constexpr uint32_t X_OFF = QF_OFF + ROWS * 4;  // Split: R, sum and Rs of both accumulators
+    static constexpr uint32_t BAR_OFF = X_OFF + (MODE == kSplit ? 2 * 3 * 128 * 4 : 0);
     static constexpr int BARS = 2 * KST + 2 * VST + 2 * DEPTH + 8 + 2;
-    static constexpr uint32_t SMEM = BAR_OFF + BARS * 8 + 8;
+    static constexpr uint32_t SMEM = BAR_OFF + BARS * 8 + 16;
     // TMEM columns: S twice, the weights' parts twice (two f16 a column), the accumulators
     static constexpr int TM_P = 2 * TN, TM_O = TM_P + TN * NP, TM_Q = TM_O + NS * D;
     // ... and, in what is left, the first QT columns of 32 f16 pairs (64 head
@@ -94,6 +99,8 @@ struct Plan {                          // in the workspace
     uint4 *entries;                    // [cap_entries], most K/V tiles first
     uint4 *items;                      // [cap_items]: seq, tile, first slot, pieces
     float *part;                       // [slots][groups][ROWS][D + 4]
+    float *sums;                       // [SMs][accumulators][128][D], or none
+    uint32_t *places;                  // a bit per place in sums: taken
     int64_t cap_items, cap_entries, cap_slots;
 };
 
@@ -179,6 +186,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
     const PrefillArgs &a = P.a;
     const int tid = threadIdx.x;
     bucket[tid] = 0;
+    if (tid < (a.num_sms + 31) / 32) P.plan.places[tid] = 0;
     if (tid == 0) sum_tiles = 0;
     uint32_t items = 0, bound = 0;                       // bound: the largest start so far
     for (int s0 = 0; s0 < a.num_seqs; s0 += kPlanThreads) {
@@ -293,6 +301,16 @@ __device__ __forceinline__ void behind32(float *v) {
     for (int k = 0; k < 32; k += 8)
         asm volatile("" : "+f"(v[k]), "+f"(v[k + 1]), "+f"(v[k + 2]), "+f"(v[k + 3]), "+f"(v[k + 4]), "+f"(v[k + 5]),
                           "+f"(v[k + 6]), "+f"(v[k + 7]));
+}
+
+// 16 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&o)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]),
+                   "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
+                 : "r"(addr) : "memory");
 }
 
 // 16 packed words into 16 columns of this thread's TMEM lane, not waited for.
@@ -457,6 +475,13 @@ __device__ __forceinline__ void store8(T *p, const float *x) {
 // needed again), t_free (the softmax warps that read the table), s_full[2]
 // (commit of QK), s_free[2] and p_full[2] (4 softmax warps), pv_done[2]
 // (commit of PV).
+//
+// The tensor cores cut an accumulator's last bit at every step, always toward
+// zero, which adds up over a long context (f32 rows, 130,000 tokens: 1.5e-4 of
+// the result, which 16-bit rows can bear).  So with f32 rows, every FLUSH jobs the softmax warps add the accumulator to f32
+// sums in the workspace and PV starts it anew.  There are as many places for sums
+// as SMs, each of which has one CTA at a time; a CTA takes a free one and gives
+// it back.
 template <typename T, typename C>
 __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     constexpr int D = C::D, TN = C::TN, CT = C::CT, SUB = C::SUB, NP = C::NP, NS = C::NS, W = C::W;
@@ -477,7 +502,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     auto pv_done = [&](int b) { return bars + 8 * (B2 + 6 + b); };
     auto drained = [&](int i) { return bars + 8 * (B2 + 8 + i); };
     volatile uint32_t *tmem_at = reinterpret_cast<volatile uint32_t *>(smem + C::BAR_OFF + C::BARS * 8);
-    volatile uint32_t *abort = tmem_at + 1;
+    volatile uint32_t *abort = tmem_at + 1, *place = tmem_at + 2;
 
     // set up while the planning kernel ends
     if (warp == 0) tmem_alloc(s0 + C::BAR_OFF + C::BARS * 8, 512);
@@ -509,6 +534,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     const int tiles = min((seen_all + CT - 1) / CT - j0, (int)P.plan.head[2]);
     const int steps = min(tiles * SUB, (seen_all + TN - 1) / TN - j0 * SUB);     // of TN tokens
     const int jobs = C::MODE == kPair ? 2 * steps : steps;
+    // whether accumulator x is flushed before the end
+    auto flushes = [&](int x) { return NP == 2 && (C::MODE == kSingle ? jobs : (jobs - x + 1) / 2) > C::FLUSH; };
+    if (flushes(0) && tid == 0) {
+        uint32_t p = 0;
+        for (int tries = 0;; p = (p + 1) % (uint32_t)a.num_sms) {
+            if (!(atomicOr(P.plan.places + p / 32, 1u << (p & 31)) >> (p & 31) & 1u)) break;
+            if (++tries > 1 << 20) {                         // never with one CTA per SM
+                *abort = 1u;
+                break;
+            }
+        }
+        __threadfence();
+        *place = p;
+    }
     const int head0 = slice * P.g.heads;                                 // first head of the kv head's group
     const int heads = min(P.g.heads, P.g.group - head0);
 
@@ -611,16 +650,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 const uint64_t aK = dK + st * (C::KV_TILE / 16) + (step % SUB) * (TN * 128 / 16);
                 const uint64_t aQ = dQ + (C::MODE == kPair ? b : 0) * (NP * C::Q_PART / 16);
                 // the small parts first: what they add is not cut at the full sum's last bit
+#pragma unroll (NP == 2 ? 1 : D / 64)
+                for (int x = 0; x < NP * (D / 64); ++x) {
+                    const int p = NP - 1 - x / (D / 64), y = x % (D / 64);
+                    const uint64_t bK = aK + y * (CT * 128 / 16);
+                    if (y < C::QT) {
+                        const uint32_t tQ = tmem + C::TM_Q + ((C::MODE == kPair ? b : 0) * NP + p) * (32 * C::QT) + 32 * y;
 #pragma unroll
-                for (int p = NP - 1; p >= 0; --p)
+                        for (int d = 0; d < 4; ++d) umma_f16_ta(tmem + b * TN, tQ + 8 * d, bK + 2 * d, ID_QK, x + d > 0);
+                    } else {
+                        const uint64_t bQ = aQ + (p * C::Q_PART + y * 128 * 128) / 16;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        if (k < 4 * C::QT)
-                            umma_f16_ta(tmem + b * TN,
-                                        tmem + C::TM_Q + ((C::MODE == kPair ? b : 0) * NP + p) * (32 * C::QT) + 8 * k,
-                                        aK + ((k >> 2) * CT * 128 + (k & 3) * 32) / 16, ID_QK, p < NP - 1 || k > 0);
-                        else umma_f16(tmem + b * TN, aQ + (p * C::Q_PART + (k >> 2) * 128 * 128 + (k & 3) * 32) / 16,
-                                 aK + ((k >> 2) * CT * 128 + (k & 3) * 32) / 16, ID_QK, p < NP - 1 || k > 0);
+                        for (int d = 0; d < 4; ++d) umma_f16(tmem + b * TN, bQ + 2 * d, bK + 2 * d, ID_QK, x + d > 0);
+                    }
+                }
                 umma_commit(s_full(b));
                 if (last && j + C::KST < tiles) umma_commit(k_free(st));
                 issued = true;
@@ -637,8 +680,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 tc_fence_after();
                 const uint64_t aV = dV + st * (C::KV_TILE / 16) + (step % SUB) * (TN * 128 / 16);
                 const uint32_t tP = tmem + C::TM_P + b * (NP * TN / 2);
-                const bool more = C::MODE == kSingle ? job > 0 : job > 1;
-#pragma unroll
+                const bool more = NP == 2 ? (C::MODE == kSingle ? job : job >> 1) % C::FLUSH != 0
+                                          : job > (C::MODE == kSingle ? 0 : 1);
+#pragma unroll (NP == 2 ? 1 : NP)
                 for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
                     for (int k = 0; k < TN / 16; ++k)
@@ -800,9 +844,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         const float qf = tiles > 0 ? reinterpret_cast<const float *>(smem + C::QF_OFF)[nt * 128 + rt] : 1.0f;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tOw = tO + (C::MODE == kSingle ? 0 : wg * D) + lanes;
-        float R = -INFINITY;
+        float R = -INFINITY, Rs = -INFINITY;                 // references of the accumulator and of the sums
         float2 l2 = make_float2(0.0f, 0.0f);
-        bool ok = true;
+        bool ok = true, flushed = false;
+        // the row's sums of accumulator x
+        auto sums_of = [&](int x) {
+            return P.plan.sums + (((int64_t)*place * NS + x) * 128 + rt) * D;
+        };
+        float *sums = flushes(0) ? sums_of(C::MODE == kSingle ? 0 : wg) : nullptr;
         auto tile_job = [&](auto mask_c, int job, int step, int b) {
             constexpr bool MASK = decltype(mask_c)::value;
             const int tab = step / SUB % C::DEPTH, sub = step % SUB;
@@ -856,20 +905,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 l2.x *= f;
                 l2.y *= f;
                 const int before = C::MODE == kSingle ? job - 1 : job - 2;   // the accumulator's last PV
-                if (before >= 0) {
+                if (before >= 0 && (NP == 1 || (C::MODE == kSingle ? job : job >> 1) % C::FLUSH != 0)) {     // (else PV starts it anew)
                     ok = wait_for(pv_done(before & 1), (before >> 1) & 1, abort);
                     if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; return; }
                     tc_fence_after();
 #pragma unroll 1
                     for (int k = 0; k < D; k += 16) {
                         float o[16];
-                        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                                     "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-                                     "tcgen05.wait::ld.sync.aligned;"
-                                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]),
-                                       "=f"(o[6]), "=f"(o[7]), "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]),
-                                       "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
-                                     : "r"(tOw + k) : "memory");
+                        tmem_ld16(tOw + k, o);
                         uint32_t u[16];
 #pragma unroll
                         for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(o[x] * f);
@@ -888,7 +931,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             float2 la = make_float2(0.0f, 0.0f), lb = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int k0 = 0; k0 < TN; k0 += 32) {
-                uint32_t hi[16], lo[16];
+                uint32_t hi[16];
+                [[maybe_unused]] uint32_t lo[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 4) {
                     const float4 v4 = *reinterpret_cast<const float4 *>(table + CT + k0 + k);
@@ -933,6 +977,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                  wait_for(s_full(b), (job >> 1) & 1, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
+            if (NP == 2 && job >= (C::MODE == kSingle ? C::FLUSH : 2 * C::FLUSH) &&
+                (C::MODE == kSingle ? job : job >> 1) % C::FLUSH == 0) {
+                // the accumulator, added to the row's sums
+                const int before = C::MODE == kSingle ? job - 1 : job - 2;
+                ok = wait_for(pv_done(before & 1), (before >> 1) & 1, abort);
+                if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+                tc_fence_after();
+                const float f = Rs == R ? 1.0f : fast_exp2(Rs - R);
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    float4 *at = reinterpret_cast<float4 *>(sums + k), s4[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) s4[x] = flushed ? at[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    tmem_ld32(tOw + k, o);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        at[x] = make_float4(fmaf(s4[x].x, f, o[4 * x]), fmaf(s4[x].y, f, o[4 * x + 1]),
+                                            fmaf(s4[x].z, f, o[4 * x + 2]), fmaf(s4[x].w, f, o[4 * x + 3]));
+                }
+                Rs = R;
+                flushed = true;
+            }
             if ((j0 * SUB + step + 1) * TN > sees_min) tile_job(std::true_type(), job, step, b);
             else tile_job(std::false_type(), job, step, b);
             if (!ok) break;
@@ -947,16 +1014,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         }
         if (!ok) *abort = 1u;
         float l = l2.x + l2.y;
-        float f0 = 1.0f, f1 = 0.0f;
+        // of the accumulators (f) and of their sums relative to them (g)
+        float f0 = 1.0f, f1 = 0.0f, g0 = Rs == R ? 1.0f : fast_exp2(Rs - R), g1 = 0.0f;
         bool both = false;
         if (C::MODE == kSplit) {
             // the two accumulators' references and sums, exchanged by the two threads of a row
             float *x = reinterpret_cast<float *>(smem + C::X_OFF);
-            x[wg * 256 + rt] = R;
-            x[wg * 256 + 128 + rt] = l;
+            x[wg * 384 + rt] = R;
+            x[wg * 384 + 128 + rt] = l;
+            x[wg * 384 + 256 + rt] = Rs;
             tc_fence_before();
             named_barrier(1, 256);
-            const float R0 = x[rt], l0 = x[128 + rt], R1 = x[256 + rt], l1 = x[384 + rt];
+            const float R0 = x[rt], l0 = x[128 + rt], R1 = x[384 + rt], l1 = x[512 + rt];
+            const float Rs0 = x[256 + rt], Rs1 = x[640 + rt];
+            g0 = Rs0 == R0 ? 1.0f : fast_exp2(Rs0 - R0);
+            g1 = Rs1 == R1 ? 1.0f : fast_exp2(Rs1 - R1);
             const float Rm = fmaxf(R0, R1);
             f0 = R0 == -INFINITY ? 0.0f : fast_exp2(R0 - Rm);
             f1 = R1 == -INFINITY ? 0.0f : fast_exp2(R1 - Rm);
@@ -980,25 +1052,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             }
             const int k_lo = C::MODE == kSplit ? wg * (D / 2) : 0, k_hi = C::MODE == kSplit ? k_lo + D / 2 : D;
 #pragma unroll 1
-            for (int k = k_lo; k < k_hi; k += 32) {
-                float o[32];
+            for (int k = k_lo; k < k_hi; k += 16) {
+                float o[16];
                 if (tiles > 0) {
-                    tmem_ld32(C::MODE == kSplit ? tO + lanes + k : tOw + k, o);
+                    const float *s0 = flushes(0) ? sums_of(C::MODE == kPair ? wg : 0) + k : nullptr;
+                    tmem_ld16(C::MODE == kSplit ? tO + lanes + k : tOw + k, o);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = l == 0.0f ? 0.0f : o[x] * f0;
+                    for (int x = 0; x < 16; ++x)
+                        o[x] = l == 0.0f ? 0.0f : (flushes(C::MODE == kPair ? wg : 0) ? fmaf(s0[x], g0, o[x]) : o[x]) * f0;
                     if (both) {
-                        float o1[32];
-                        tmem_ld32(tO + D + lanes + k, o1);
+                        const float *s1 = flushes(1) ? sums_of(1) + k : nullptr;
+                        float o1[16];
+                        tmem_ld16(tO + D + lanes + k, o1);
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) o[x] += l == 0.0f ? 0.0f : o1[x] * f1;
+                        for (int x = 0; x < 16; ++x)
+                            o[x] += l == 0.0f ? 0.0f : (flushes(1) ? fmaf(s1[x], g1, o1[x]) : o1[x]) * f1;
                     }
                 } else {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+                    for (int x = 0; x < 16; ++x) o[x] = 0.0f;
                 }
                 if (row_ok) {
 #pragma unroll
-                    for (int x = 0; x < 32; x += 8) {
+                    for (int x = 0; x < 16; x += 8) {
                         if (piece) store8(rec + k + x, o + x);
                         else store8(dst + k + x, o + x);
                     }
@@ -1018,6 +1094,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     if (warp == 0) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+    if (tid == 0 && flushes(0)) {
+        __threadfence();                                     // the sums' last readers are behind the barrier
+        atomicAnd(P.plan.places + *place / 32, ~(1u << (*place & 31)));
     }
     if (failed && tid == 0) flag_error(a.status, kDevWaitTimeout);
 }
@@ -1119,6 +1199,11 @@ size_t layout(const PrefillArgs &a, Params &P) {
     p.entries = reinterpret_cast<uint4 *>(take((size_t)p.cap_entries * 16));
     p.items = reinterpret_cast<uint4 *>(take(P.may_split ? (size_t)p.cap_items * 16 : 0));
     p.part = reinterpret_cast<float *>(take((size_t)p.cap_slots * g.groups * P.rows * (a.head_size + 4) * 4));
+    p.places = reinterpret_cast<uint32_t *>(take((size_t)(a.num_sms + 31) / 32 * 4));
+    // (a context short of the shortest flush needs no sums)
+    const bool sums = (int64_t)a.max_blocks_per_seq * a.block_size > kFlush * kTN;
+    p.sums = reinterpret_cast<float *>(
+        take(sums ? (size_t)a.num_sms * (a.head_size == 256 ? 1 : 2) * 128 * a.head_size * 4 : 0));
     return at;
 }
 

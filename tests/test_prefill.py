@@ -151,6 +151,35 @@ def test_long_prompt(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("H,Hk,D,rows,ctx", [(16, 8, 128, 500, 40000), (4, 2, 64, 700, 30000), (16, 1, 256, 400, 30000),
+                                             (32, 8, 128, 5000, 9000)])
+def test_f32_sums_over_long_contexts(H, Hk, D, rows, ctx):
+    """V with a mean, so that every term adds up.  An accumulator of the tensor cores loses half a last
+    bit (2^-24 of itself) on average at each of its at most 32 x 8 steps, 1.5e-5 of it in all at most;
+    the bound is 2e-5 of the result (2-norm).  Without sums of its
+    own, 30,000 tokens are 3,750 steps and more: over 1e-4."""
+    import torch
+    from tests.gpu_helpers import device_status
+    c = Case(H, Hk, D, 16, [ctx, 100], [rows, 100], seed=D)
+    words = c.vc.clone()
+    codes = words[..., :-1].contiguous().view(torch.int8)
+    words[..., :-1] = (codes // 2 + 60).to(torch.int8).view(torch.int32)        # codes -4 .. 123
+    c.vc.copy_(words)
+    got = c.run().double()
+    k, v = (x[c.bt[0].long()].permute(1, 0, 2, 3).reshape(Hk, -1, D // 4 + 1)[:, :ctx] for x in (c.kc, c.vc))
+    k, v = (x[..., :-1].contiguous().view(torch.int8).double() * x[..., -1:].contiguous().view(torch.float32).double()
+            for x in (k, v))
+    at = torch.arange(0, rows, max(1, rows // 60), device="cuda")               # some of the rows
+    q = c.q[at].double().view(len(at), Hk, H // Hk, D)
+    z = torch.einsum("ighd,gtd->ight", q, k) * c.w.scale
+    seen = torch.arange(ctx, device="cuda")[None] < ctx - (rows - 1 - at)[:, None]
+    p = torch.softmax(z.masked_fill(~seen[:, None, None], -np.inf), -1)
+    want = torch.einsum("ight,gtd->ighd", p, v).reshape(len(at), H, D)
+    assert float((got[at] - want).norm() / want.norm()) <= 2e-5
+    assert device_status() == 0
+
+
+@gpu
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_a_row_per_sequence_is_the_decode(D):
     """One row per sequence: the definition is pa_q8_decode's."""
