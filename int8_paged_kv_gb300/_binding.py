@@ -436,42 +436,45 @@ def pa_q8c_decode(out, q, key_cache, value_cache, context_lens, *, num_kv_heads:
     return out
 
 
+_U32 = ()                   # dtypes of u32 buffers (the same bits), and two of torch's calls, once it is loaded
+_current_device = _raw_stream = None
+
+
 def _address(t, dtypes, name, device, numel=-1):
     """Address of a contiguous CUDA tensor of one of the given types on the
     device with this index, with the number of elements asked for."""
+    if t.dtype in dtypes and t.get_device() == device and t.is_contiguous() and (numel < 0 or t.numel() == numel):
+        return t.data_ptr()
     if t.dtype not in dtypes or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor of dtype {' or '.join(map(str, dtypes))}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel >= 0 and t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    return t.data_ptr()
-
-
-def _u32():
-    import torch
-    return torch.int32, torch.uint32            # the same bits
+    raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
 
 
 def _current(t):
     """Index of the tensor's device, which has to be the current one: the
     library queues there."""
-    import torch
-    if not t.is_cuda:
-        raise TypeError("tensors must be CUDA tensors")
+    global _U32, _current_device, _raw_stream
+    if _current_device is None:
+        import torch
+        _U32 = (torch.int32, torch.uint32)
+        _raw_stream = torch._C._cuda_getCurrentRawStream
+        _current_device = torch.cuda.current_device
     device = t.get_device()
-    if device != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if device < 0:
+        raise TypeError("tensors must be CUDA tensors")
+    if device != _current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{_current_device()}")
     return device
 
 
 def _queue(stream, device):
     """The stream's handle (None: the device's current stream)."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -531,7 +534,7 @@ def pa_q8_prefill(out, q, key_cache, value_cache, block_tables, context_lens, qu
     nb = int(key_cache.shape[0]) if num_blocks is None else int(num_blocks)
     if nb * num_kv_heads * block_size * (D // 4 + 1) > words:
         raise ValueError("the caches do not hold num_blocks pages of these sizes")
-    u32 = _u32()
+    u32 = _U32
     L = lib()
     need = L.pa_q8_prefill_workspace_size(T, S, H, num_kv_heads, D, block_size, Nb, dt)
     ws, ws_bytes = _scratch(need, workspace, q, stream)
@@ -553,7 +556,8 @@ def _copy_blocks(fn, key_cache, value_cache, src_blocks, dst_blocks, dtypes, hea
             raise ValueError("the caches do not hold num_blocks pages")
         nb = int(num_blocks)
     n = src_blocks.numel()
-    u32 = _u32()
+    u32 = _U32
+    dtypes = dtypes or u32
     _check(fn, getattr(lib(), fn)(
         _address(key_cache, dtypes, "key_cache", dev), _address(value_cache, dtypes, "value_cache", dev),
         _address(src_blocks, u32, "src_blocks", dev), _address(dst_blocks, u32, "dst_blocks", dev, n),
@@ -563,7 +567,7 @@ def _copy_blocks(fn, key_cache, value_cache, src_blocks, dst_blocks, dtypes, hea
 def pa_q8_copy_blocks(key_cache, value_cache, src_blocks, dst_blocks, *, num_blocks: int | None = None,
                       stream=None) -> None:
     """Copy page src_blocks[i] to dst_blocks[i] of both q8 caches (0xFFFFFFFF: no pair)."""
-    _copy_blocks("pa_q8_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, _u32(),
+    _copy_blocks("pa_q8_copy_blocks", key_cache, value_cache, src_blocks, dst_blocks, None,
                  4 * (key_cache.shape[-1] - 1), num_blocks, stream)
 
 
@@ -584,7 +588,7 @@ def _pool(block_tables, context_lens, ref_counts, free_blocks, num_free):
     dev = _current(block_tables)
     S, Nb = block_tables.shape
     nb = ref_counts.numel()
-    u32 = _u32()
+    u32 = _U32
     return dev, S, Nb, nb, (
         _address(block_tables, u32, "block_tables", dev), _address(context_lens, u32, "context_lens", dev, S),
         _address(ref_counts, u32, "ref_counts", dev), _address(free_blocks, u32, "free_blocks", dev, nb),
@@ -594,7 +598,7 @@ def _pool(block_tables, context_lens, ref_counts, free_blocks, num_free):
 def pa_q8_pool_init(ref_counts, free_blocks, num_free, *, stream=None) -> None:
     """All pages of the pool free (see include/pa_q8.h)."""
     dev, nb = _current(ref_counts), ref_counts.numel()
-    u32 = _u32()
+    u32 = _U32
     _check("pa_q8_pool_init", lib().pa_q8_pool_init(
         _address(ref_counts, u32, "ref_counts", dev), _address(free_blocks, u32, "free_blocks", dev, nb),
         _address(num_free, u32, "num_free", dev, 1), nb, _queue(stream, dev)))
@@ -606,7 +610,7 @@ def pa_q8_extend_seqs(block_tables, context_lens, ref_counts, free_blocks, num_f
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     n = seqs.numel()
     L = lib()
-    u32 = _u32()
+    u32 = _U32
     ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
     _check("pa_q8_extend_seqs", L.pa_q8_extend_seqs(
         *pool, _address(seqs, u32, "seqs", dev), _address(new_lens, u32, "new_lens", dev, n), n, S, Nb,
@@ -620,7 +624,7 @@ def pa_q8_fork_seqs(block_tables, context_lens, ref_counts, free_blocks, num_fre
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     n = parents.numel()
     L = lib()
-    u32 = _u32()
+    u32 = _U32
     ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
     _check("pa_q8_fork_seqs", L.pa_q8_fork_seqs(
         *pool, _address(parents, u32, "parents", dev), _address(children, u32, "children", dev, n),
@@ -633,7 +637,7 @@ def pa_q8_free_seqs(block_tables, context_lens, ref_counts, free_blocks, num_fre
     """Empty the rows seqs[i]; pages that no row holds go back to the pool."""
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     _check("pa_q8_free_seqs", lib().pa_q8_free_seqs(
-        *pool, _address(seqs, _u32(), "seqs", dev), seqs.numel(), S, Nb, block_size, nb, _queue(stream, dev)))
+        *pool, _address(seqs, _U32, "seqs", dev), seqs.numel(), S, Nb, block_size, nb, _queue(stream, dev)))
 
 
 def pa_q8_compact_blocks(block_tables, context_lens, ref_counts, free_blocks, num_free, move_src, move_dst, *,
@@ -643,7 +647,7 @@ def pa_q8_compact_blocks(block_tables, context_lens, ref_counts, free_blocks, nu
     dev, S, Nb, nb, pool = _pool(block_tables, context_lens, ref_counts, free_blocks, num_free)
     n = move_src.numel()
     L = lib()
-    u32 = _u32()
+    u32 = _U32
     ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, 0), workspace, block_tables, stream)
     _check("pa_q8_compact_blocks", L.pa_q8_compact_blocks(
         *pool, _address(move_src, u32, "move_src", dev), _address(move_dst, u32, "move_dst", dev, n), n, S, Nb,

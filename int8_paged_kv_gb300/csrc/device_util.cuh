@@ -12,9 +12,6 @@ constexpr uint32_t kPadSlot = 0xFFFFFFFFu;
 constexpr uint32_t kDevBadBlock = 0x1u;
 constexpr uint32_t kDevBadSlot = 0x2u;
 constexpr uint32_t kDevWaitTimeout = 0x4u;
-constexpr uint32_t kDevBadSeq = 0x8u;
-constexpr uint32_t kDevNoBlock = 0x10u;
-constexpr uint32_t kDevBadRows = 0x20u;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // a stage wait normally takes microseconds
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {

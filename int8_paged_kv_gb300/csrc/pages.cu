@@ -19,6 +19,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kPlanThreads = 1024;
+constexpr int kRowThreads = 256;                         // of a CTA that walks one row, four entries a thread
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 // A page whose count reached zero in this call carries this mark until the
 // stack takes it.  The mark and every correction are additions, so they
@@ -30,37 +31,88 @@ constexpr uint32_t kOver = 0x20000000u;
 
 // ------------------------------------------------------------ page copies
 
-constexpr int kCopyThreads = 256;
-constexpr int kCopyBatch = 4;                            // 16-byte loads in flight per thread
+constexpr int kCopyPiece = 16384;                        // most bytes of one bulk copy
+constexpr int kCopyStages = 4, kCopyAhead = 2;           // buffers of a CTA; loads it has under way
+constexpr int kCopyPerSm = 3;                            // CTAs of one warp
+constexpr int kCopyLists = 4;                            // list entries that a lane looks up at once
 
-// Pair p copies page src[p] to dst[p] of both caches.  Units of
-// kCopyThreads * kCopyBatch * 16 bytes (16 KB) go round the grid.
-__global__ void __launch_bounds__(kCopyThreads)
-copy_pages_kernel(uint4 *key, uint4 *value, const uint32_t *src, const uint32_t *dst, int64_t pairs,
-                  int64_t page_vecs, int64_t num_blocks, uint32_t *status) {
-    constexpr int kUnit = kCopyThreads * kCopyBatch;
-    const int64_t pieces = (page_vecs + kUnit - 1) / kUnit;
-    const int64_t units = pairs * 2 * pieces;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int64_t p = u / (2 * pieces);
-        const int64_t r = u - p * 2 * pieces;
-        const uint32_t s = src[p], d = dst[p];
-        if (s == kNone || d == kNone) continue;
-        if (s >= num_blocks || d >= num_blocks) {
-            if (threadIdx.x == 0) flag_error(status, kDevBadBlock);
-            continue;
+__device__ __forceinline__ void bulk_copy_s2g(void *dst, uint32_t src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Pair p copies page src[p] to dst[p] of both caches.  A unit is one page of
+// one cache, cut into equal pieces of at most kCopyPiece bytes that go through
+// a ring of shared-memory buffers, in and out by bulk copies: no register
+// holds a byte, and a CTA keeps kCopyAhead pieces under way.  Units go round
+// the grid; a lane looks up four of them at a time, so that a list's padding
+// costs one round of loads per 128 units of a CTA.
+__global__ void __launch_bounds__(32)
+copy_pages_kernel(char *key, char *value, const uint32_t *src, const uint32_t *dst, int64_t pairs,
+                  int64_t page_bytes, uint32_t piece_bytes, int64_t num_blocks, uint32_t *status) {
+    extern __shared__ __align__(128) char buffers[];
+    __shared__ uint64_t bars[kCopyStages];
+    __shared__ struct { char *to; uint32_t bytes; } place[kCopyStages];
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < kCopyStages; ++i) mbar_init(smem_addr(bars + i), 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    const uint64_t policy = l2_policy_evict_first();
+    uint32_t loads = 0, stores = 0;                      // lane 0's
+    bool ok = true;
+    auto store_next = [&]() {
+        const uint32_t st = stores % kCopyStages;
+        ok = ok && mbar_wait(smem_addr(bars + st), stores / kCopyStages & 1);
+        if (ok) bulk_copy_s2g(place[st].to, smem_addr(buffers + st * piece_bytes), place[st].bytes);
+        ++stores;
+    };
+    const int64_t units = 2 * pairs;
+    for (int64_t u0 = blockIdx.x; u0 < units; u0 += (int64_t)gridDim.x * 32 * kCopyLists) {
+        uint32_t s[kCopyLists], d[kCopyLists];
+#pragma unroll
+        for (int k = 0; k < kCopyLists; ++k) {
+            const int64_t u = u0 + (int64_t)gridDim.x * (32 * k + lane);
+            s[k] = u < units ? src[u >> 1] : kNone;
+            d[k] = u < units ? dst[u >> 1] : kNone;
         }
-        uint4 *base = r < pieces ? key : value;
-        const int64_t v0 = (r < pieces ? r : r - pieces) * kUnit + threadIdx.x;
-        const uint4 *from = base + (int64_t)s * page_vecs;
-        uint4 *to = base + (int64_t)d * page_vecs;
-        uint4 x[kCopyBatch];
 #pragma unroll
-        for (int k = 0; k < kCopyBatch; ++k)
-            if (v0 + k * kCopyThreads < page_vecs) x[k] = from[v0 + k * kCopyThreads];
-#pragma unroll
-        for (int k = 0; k < kCopyBatch; ++k)
-            if (v0 + k * kCopyThreads < page_vecs) to[v0 + k * kCopyThreads] = x[k];
+        for (int k = 0; k < kCopyLists; ++k) {
+            bool good = s[k] != kNone && d[k] != kNone;
+            if (good && (s[k] >= num_blocks || d[k] >= num_blocks)) {
+                flag_error(status, kDevBadBlock);
+                good = false;
+            }
+            for (uint32_t left = __ballot_sync(0xFFFFFFFFu, good); left; left &= left - 1) {
+                const int l = __ffs(left) - 1;
+                const int64_t from = (int64_t)__shfl_sync(0xFFFFFFFFu, s[k], l) * page_bytes;
+                const int64_t to = (int64_t)__shfl_sync(0xFFFFFFFFu, d[k], l) * page_bytes;
+                if (lane != 0) continue;
+                char *base = (u0 + (int64_t)gridDim.x * (32 * k + l)) & 1 ? value : key;
+                for (int64_t at = 0; at < page_bytes && ok; at += piece_bytes) {
+                    const uint32_t st = loads % kCopyStages, bar = smem_addr(bars + st);
+                    const uint32_t bytes = (uint32_t)min((int64_t)piece_bytes, page_bytes - at);
+                    // the buffer's last store, kCopyStages pieces ago, has read it
+                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kCopyStages - kCopyAhead - 1) : "memory");
+                    place[st].to = base + to + at;
+                    place[st].bytes = bytes;
+                    mbar_arrive_expect_tx(bar, bytes);
+                    bulk_copy_g2s(smem_addr(buffers + st * piece_bytes), base + from + at, bytes, bar, policy);
+                    if (++loads - stores > kCopyAhead) store_next();
+                }
+            }
+        }
+    }
+    if (lane == 0) {
+        while (stores != loads) store_next();
+        if (!ok) {
+            flag_error(status, kDevWaitTimeout);
+            for (int i = 0; i < kCopyStages; ++i)        // what is still under way writes to this CTA's memory
+                if (loads > (uint32_t)i) mbar_wait(smem_addr(bars + i), (loads - 1 - i) / kCopyStages & 1);
+        }
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 }
 
@@ -71,6 +123,20 @@ __device__ __forceinline__ uint32_t tokens_of(const PoolArgs &a, uint32_t seq) {
 }
 __device__ __forceinline__ uint32_t pages_of(const PoolArgs &a, uint32_t tokens) {
     return (tokens + a.block_size - 1) / a.block_size;
+}
+
+// f(j, get(j)) for the entries j < n of one row, by a CTA of kRowThreads with
+// four loads in flight per thread.
+template <typename G, typename F>
+__device__ __forceinline__ void for_entries(uint32_t n, G get, F f) {
+    for (uint32_t j0 = threadIdx.x; j0 < n; j0 += kRowThreads * 4) {
+        uint32_t b[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[k] = j0 + kRowThreads * k < n ? get(j0 + kRowThreads * k) : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j0 + kRowThreads * k < n) f(j0 + kRowThreads * k, b[k]);
+    }
 }
 
 // Exclusive sum of x over the CTA's kPlanThreads threads, and its total.
@@ -169,7 +235,7 @@ fork_plan_kernel(PoolArgs a, const uint32_t *parents, const uint32_t *children, 
     if (threadIdx.x == 0) *a.num_free = top - (uint32_t)min(base, (unsigned long long)top);
 }
 
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kRowThreads)
 fork_rows_kernel(PoolArgs a, const uint32_t *parents, const uint32_t *children, const uint2 *info) {
     grid_dependency_wait();
     const uint2 t = info[blockIdx.x];
@@ -177,12 +243,11 @@ fork_rows_kernel(PoolArgs a, const uint32_t *parents, const uint32_t *children, 
     const uint32_t *from = a.block_tables + (int64_t)parents[blockIdx.x] * a.max_blocks_per_seq;
     uint32_t *to = a.block_tables + (int64_t)children[blockIdx.x] * a.max_blocks_per_seq;
     const uint32_t whole = t.x / a.block_size;
-    for (uint32_t j = threadIdx.x; j < whole; j += blockDim.x) {
-        const uint32_t b = from[j];
+    for_entries(whole, [&](uint32_t j) { return from[j]; }, [&](uint32_t j, uint32_t b) {
         to[j] = b;
         if (b < a.num_blocks) atomicAdd(a.ref_counts + b, 1u);
         else flag_error(a.status, kDevBadBlock);
-    }
+    });
     if (threadIdx.x == 0 && t.x % a.block_size) {
         to[whole] = t.y;
         if (t.y < a.num_blocks) a.ref_counts[t.y] = 1;
@@ -231,39 +296,41 @@ extend_plan_kernel(PoolArgs a, const uint32_t *seqs, const uint32_t *new_lens, i
     if (threadIdx.x == 0) *a.num_free = top - (uint32_t)taken;
 }
 
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kRowThreads)
 extend_rows_kernel(PoolArgs a, const uint32_t *seqs, const uint4 *info) {
     grid_dependency_wait();
     const uint4 t = info[blockIdx.x];
     if (!t.y) return;
     uint32_t *row = a.block_tables + (int64_t)seqs[blockIdx.x] * a.max_blocks_per_seq + t.x;
-    for (uint32_t k = threadIdx.x; k < t.y; k += blockDim.x) {
-        const uint32_t b = a.free_blocks[t.z - 1 - k];
+    for_entries(t.y, [&](uint32_t k) { return a.free_blocks[t.z - 1 - k]; }, [&](uint32_t k, uint32_t b) {
         row[k] = b;
         if (b < a.num_blocks) a.ref_counts[b] = 1;
         else flag_error(a.status, kDevBadBlock);
-    }
+    });
 }
 
-// ---- free: one count less per page held; a row named twice is freed once.
-__global__ void __launch_bounds__(256) free_rows_kernel(PoolArgs a, const uint32_t *seqs, int n) {
-    const int i = blockIdx.x;
-    const uint32_t s = seqs[i];
+// ---- free: one count less per page held.  A row's length is exchanged for
+// zero by the request that frees it: named twice, it has no pages the second
+// time.
+__global__ void __launch_bounds__(kRowThreads) free_rows_kernel(PoolArgs a, const uint32_t *seqs) {
+    __shared__ uint32_t pages;
+    const uint32_t s = seqs[blockIdx.x];
     grid_dependents_launch();
     if (s >= (uint32_t)a.num_seqs) {
         if (threadIdx.x == 0) flag_error(a.status, kDevBadSeq);
         return;
     }
-    bool again = false;
-    for (int j = threadIdx.x; j < i; j += blockDim.x) again |= seqs[j] == s;
-    if (__syncthreads_or(again)) return;
-    const uint32_t held = pages_of(a, tokens_of(a, s));
+    if (threadIdx.x == 0) {
+        const uint32_t len = atomicExch(a.context_lens + s, 0u);
+        pages = pages_of(a, (uint32_t)min((int64_t)len, (int64_t)a.max_blocks_per_seq * a.block_size));
+    }
+    __syncthreads();
+    const uint32_t held = pages;
     const uint32_t *row = a.block_tables + (int64_t)s * a.max_blocks_per_seq;
-    for (uint32_t j = threadIdx.x; j < held; j += blockDim.x) {
-        const uint32_t b = row[j];
+    for_entries(held, [&](uint32_t j) { return row[j]; }, [&](uint32_t, uint32_t b) {
         if (b >= a.num_blocks) {
             flag_error(a.status, kDevBadBlock);
-            continue;
+            return;
         }
         const uint32_t old = atomicSub(a.ref_counts + b, 1u);
         if (old == 0 || old >= kOver) {
@@ -272,9 +339,7 @@ __global__ void __launch_bounds__(256) free_rows_kernel(PoolArgs a, const uint32
         } else if (old == 1) {
             atomicAdd(a.ref_counts + b, kFreedMark);
         }
-    }
-    __syncthreads();                                     // the length was read
-    if (threadIdx.x == 0) a.context_lens[s] = 0;
+    });
 }
 
 // The exclusive sum over a cluster's CTAs of per-CTA counts, and the total:
@@ -384,17 +449,16 @@ compact_plan_kernel(PoolArgs a, uint32_t *move_src, uint32_t *move_dst, int64_t 
     if (cl.block_rank() == 0 && threadIdx.x == 0) *a.num_free = (uint32_t)(a.num_blocks - live);
 }
 
-__global__ void __launch_bounds__(256) compact_rows_kernel(PoolArgs a, const uint32_t *remap) {
+__global__ void __launch_bounds__(kRowThreads) compact_rows_kernel(PoolArgs a, const uint32_t *remap) {
     grid_dependency_wait();
     const uint32_t live = (uint32_t)a.num_blocks - *a.num_free;
     for (int s = blockIdx.x; s < a.num_seqs; s += gridDim.x) {
         uint32_t *row = a.block_tables + (int64_t)s * a.max_blocks_per_seq;
         const uint32_t held = pages_of(a, tokens_of(a, s));
-        for (uint32_t j = threadIdx.x; j < held; j += blockDim.x) {
-            const uint32_t b = row[j];
+        for_entries(held, [&](uint32_t j) { return row[j]; }, [&](uint32_t j, uint32_t b) {
             if (b >= a.num_blocks) flag_error(a.status, kDevBadBlock);
             else if (b >= live) row[j] = remap[b];
-        }
+        });
     }
 }
 
@@ -426,12 +490,16 @@ size_t pool_workspace_bytes(int num_seqs, int64_t num_blocks, int num_requests) 
 cudaError_t launch_copy_pages(uint32_t *key, uint32_t *value, const uint32_t *src, const uint32_t *dst, int64_t pairs,
                               int64_t page_bytes, int64_t num_blocks, int num_sms, uint32_t *status,
                               cudaStream_t st) {
-    const int64_t vecs = page_bytes / 16, unit = kCopyThreads * kCopyBatch;
-    const int64_t units = pairs * 2 * ((vecs + unit - 1) / unit);
-    const int64_t grid = units < num_sms * 8 ? units : num_sms * 8;
-    copy_pages_kernel<<<(unsigned)grid, kCopyThreads, 0, st>>>(reinterpret_cast<uint4 *>(key),
-                                                               reinterpret_cast<uint4 *>(value), src, dst, pairs,
-                                                               vecs, num_blocks, status);
+    const int64_t pieces = (page_bytes + kCopyPiece - 1) / kCopyPiece;
+    const uint32_t piece = (uint32_t)(((page_bytes + pieces - 1) / pieces + 15) / 16 * 16);
+    const int64_t most = (int64_t)num_sms * kCopyPerSm;
+    const unsigned grid = (unsigned)(pairs * 2 < most ? pairs * 2 : most);
+    const int smem = (int)(piece * kCopyStages);
+    cudaError_t e = cudaFuncSetAttribute(copy_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kCopyPiece * kCopyStages);
+    if (e != cudaSuccess) return e;
+    copy_pages_kernel<<<grid, 32, smem, st>>>(reinterpret_cast<char *>(key), reinterpret_cast<char *>(value), src, dst,
+                                              pairs, page_bytes, piece, num_blocks, status);
     return cudaGetLastError();
 }
 
@@ -447,7 +515,7 @@ cudaError_t launch_fork(const PoolArgs &a, const uint32_t *parents, const uint32
     uint32_t *claim = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + up16((size_t)n * sizeof(uint4)));
     fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, parents, children, n, copy_src, copy_dst, claim, info);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_after(fork_rows_kernel, dim3(n), 128, st, a, parents, children,
+    return e != cudaSuccess ? e : launch_after(fork_rows_kernel, dim3(n), kRowThreads, st, a, parents, children,
                                                static_cast<const uint2 *>(info));
 }
 
@@ -457,12 +525,12 @@ cudaError_t launch_extend(const PoolArgs &a, const uint32_t *seqs, const uint32_
     uint32_t *claim = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + up16((size_t)n * sizeof(uint4)));
     extend_plan_kernel<<<1, kPlanThreads, 0, st>>>(a, seqs, new_lens, n, claim, info);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_after(extend_rows_kernel, dim3(n), 128, st, a, seqs,
+    return e != cudaSuccess ? e : launch_after(extend_rows_kernel, dim3(n), kRowThreads, st, a, seqs,
                                                static_cast<const uint4 *>(info));
 }
 
 cudaError_t launch_free(const PoolArgs &a, const uint32_t *seqs, int n, cudaStream_t st) {
-    free_rows_kernel<<<n, 256, 0, st>>>(a, seqs, n);
+    free_rows_kernel<<<n, kRowThreads, 0, st>>>(a, seqs);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_after(free_push_kernel, dim3(kCluster), kPlanThreads, st, a);
 }
@@ -473,7 +541,7 @@ cudaError_t launch_compact(const PoolArgs &a, uint32_t *move_src, uint32_t *move
     compact_plan_kernel<<<kCluster, kPlanThreads, 0, st>>>(a, move_src, move_dst, capacity, remap);
     const cudaError_t e = cudaGetLastError();
     const int grid = a.num_seqs < 1024 ? a.num_seqs : 1024;
-    return e != cudaSuccess ? e : launch_after(compact_rows_kernel, dim3(grid), 256, st, a,
+    return e != cudaSuccess ? e : launch_after(compact_rows_kernel, dim3(grid), kRowThreads, st, a,
                                                static_cast<const uint32_t *>(remap));
 }
 
