@@ -3,11 +3,18 @@
 //
 // The pool operators are whole-number bookkeeping over a few hundred KB that
 // sits in L2, so their time is launches and dependent loads, not bytes.  Each
-// is one or two launches: a planning CTA that decides for all requests in
-// order (a scan), then a CTA per request that touches the tables.  Results do
-// not depend on the order in which CTAs run: every decision that depends on
-// other requests is a scan over the request index or the page number, and
-// the only atomics are whole-number sums and minima.
+// is two launches, the second queued so that it may begin while the first one
+// drains: decisions that depend on other requests are scans (over the request
+// index in one CTA, over the page numbers in a cluster of eight), and a CTA
+// per row walks the block tables.  Results do not depend on the order in which
+// CTAs run: the only atomics are whole-number sums, minima and exchanges.
+//
+// Replayed in a CUDA graph behind a copy that puts the tables back, for 256
+// sequences of up to 8192 tokens in a pool of 52,000 pages of 16: fork of 128
+// and the copy of their open pages 12.3 us, free and extend of 128 together
+// 16.4 us; of one, among 64 sequences of up to 4096 tokens, 14.4 us.  (Both launches of an operator as one of a single
+// cluster, tables walked by its 256 warps: 4-5 us less on the host for each
+// operator, but 2-4 us more on the GPU for one request and 6-8 us for 128.)
 #include <cooperative_groups.h>
 
 #include "device_util.cuh"
@@ -48,6 +55,12 @@ __device__ __forceinline__ void bulk_copy_s2g(void *dst, uint32_t src, uint32_t 
 // holds a byte, and a CTA keeps kCopyAhead pieces under way.  Units go round
 // the grid; a lane looks up four of them at a time, so that a list's padding
 // costs one round of loads per 128 units of a CTA.
+//
+// Bound by HBM: 8192 pairs of 16,896-byte pages, 554 MB read and written, take
+// 92 us (6.0 TB/s); in a list of 24,576 with the other entries empty, 92 us.
+// (Through registers, four 16-byte loads per thread: 99 and 128 us.  Pieces of
+// at most 4, 8, 16 and 32 KB: 95, 94, 92 and 92 us; one CTA per SM 94-134 us,
+// two or three 92.)  Few pairs cost a launch: 4.1 us for five.
 __global__ void __launch_bounds__(32)
 copy_pages_kernel(char *key, char *value, const uint32_t *src, const uint32_t *dst, int64_t pairs,
                   int64_t page_bytes, uint32_t piece_bytes, int64_t num_blocks, uint32_t *status) {
@@ -342,97 +355,126 @@ __global__ void __launch_bounds__(kRowThreads) free_rows_kernel(PoolArgs a, cons
     });
 }
 
-// The exclusive sum over a cluster's CTAs of per-CTA counts, and the total:
-// every CTA writes its count into rank 0..7's table through shared memory.
+// The page numbers are cut into one run per warp of a cluster of eight CTAs.
+// A warp counts its run with ballots, the counts of all go into a table in
+// every CTA through distributed shared memory, and each warp adds up the ones
+// before its own: one exchange, and no barrier inside a run.  (Sweeps of a
+// whole CTA with a scan after each: 12.5 us against 6.3 for
+// what a free puts back and 20 against 11 for a compaction's plan, in a pool of
+// 52,000 pages.)
 constexpr int kCluster = 8;
-__device__ uint32_t scan_cluster(cg::cluster_group &cl, uint32_t mine, uint32_t &total) {
-    __shared__ uint32_t counts[kCluster];
-    cl.sync();                                           // the table is free in every CTA
-    if (threadIdx.x < kCluster) *cl.map_shared_rank(&counts[cl.block_rank()], threadIdx.x) = mine;
-    cl.sync();
-    uint32_t before = 0;
-    total = 0;
-    for (int r = 0; r < kCluster; ++r) {
-        if (r < (int)cl.block_rank()) before += counts[r];
-        total += counts[r];
-    }
-    return before;
+constexpr int kRuns = kCluster * kPlanThreads / 32;
+
+struct Run {
+    int id;
+    int64_t lo, hi, per;
+};
+__device__ __forceinline__ Run run_of(const cg::cluster_group &cl, int64_t num_blocks) {
+    Run r;
+    r.id = (int)cl.block_rank() * (kPlanThreads / 32) + (threadIdx.x >> 5);
+    r.per = (num_blocks + kRuns * 32 - 1) / (kRuns * 32) * 32;
+    r.lo = min(num_blocks, r.per * r.id);
+    r.hi = min(num_blocks, r.lo + r.per);
+    return r;
 }
 
-// A CTA's share of the pages, in whole sweeps of its threads.
-__device__ __forceinline__ void share_of(int64_t num_blocks, int rank, int64_t &lo, int64_t &hi) {
-    const int64_t per = (num_blocks + kCluster * (int64_t)kPlanThreads - 1) / (kCluster * (int64_t)kPlanThreads) *
-                        kPlanThreads;
-    lo = min(num_blocks, per * rank);
-    hi = min(num_blocks, lo + per);
+// f(page, its count, warp-wide) for the pages [lo, hi) in steps of 32, four
+// loads in flight; lanes behind hi get count 0 and page >= hi.
+template <typename F>
+__device__ __forceinline__ void for_pages(const uint32_t *ref_counts, int64_t lo, int64_t hi, F f) {
+    for (int64_t b0 = lo + (threadIdx.x & 31); b0 - (threadIdx.x & 31) < hi; b0 += 128) {
+        uint32_t c[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = b0 + 32 * k < hi ? ref_counts[b0 + 32 * k] : 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f(b0 + 32 * k, c[k]);
+    }
+}
+
+// Puts a run's count into the table of every CTA.  The cluster's CTAs have all
+// arrived at its barrier once before.
+__device__ __forceinline__ void share_count(cg::cluster_group &cl, uint32_t *counts, int id, uint32_t mine) {
+    const int lane = threadIdx.x & 31;
+    cl.barrier_wait();                                   // every CTA runs
+    if (lane < kCluster) *cl.map_shared_rank(&counts[id], lane) = mine;
+    cl.sync();
+}
+
+// The sum of the counts of the runs before run `id`.
+__device__ __forceinline__ uint32_t count_before(const uint32_t *counts, int id) {
+    uint32_t sum = 0;
+    for (int r = threadIdx.x & 31; r < id; r += 32) sum += counts[r];
+    return __reduce_add_sync(0xFFFFFFFFu, sum);
 }
 
 // The pages freed in this call go onto the stack, lowest number first.
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads) free_push_kernel(PoolArgs a) {
-    grid_dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
-    int64_t lo, hi;
-    share_of(a.num_blocks, cl.block_rank(), lo, hi);
+    cl.barrier_arrive();
+    const Run run = run_of(cl, a.num_blocks);
+    const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
+    grid_dependency_wait();
     const uint32_t top = (uint32_t)min((int64_t)*a.num_free, a.num_blocks);
-    uint32_t n = 0;
-    for (int64_t b = lo + threadIdx.x; b < hi; b += kPlanThreads) n += a.ref_counts[b] == kFreedMark;
-    unsigned long long mine;
-    scan_cta(n, mine);
-    uint32_t total;
-    uint32_t at = top + scan_cluster(cl, (uint32_t)mine, total);
-    for (int64_t b0 = lo; b0 < hi; b0 += kPlanThreads) {
-        const int64_t b = b0 + threadIdx.x;
-        const bool freed = b < hi && a.ref_counts[b] == kFreedMark;
-        unsigned long long here;
-        const unsigned long long k = scan_cta(freed, here);
-        if (freed) {
-            a.ref_counts[b] = 0;
-            if (at + k < a.num_blocks) a.free_blocks[at + k] = (uint32_t)b;
-            else flag_error(a.status, kDevBadBlock);     // more free pages than the pool has
-        }
-        at += (uint32_t)here;
+    __shared__ uint32_t counts[kRuns];
+    uint32_t mine = 0;
+    for_pages(a.ref_counts, run.lo, run.hi, [&](int64_t, uint32_t c) {
+        mine += __popc(__ballot_sync(0xFFFFFFFFu, c == kFreedMark));
+    });
+    share_count(cl, counts, run.id, mine);               // (and every CTA has read the top)
+    uint32_t at = top + count_before(counts, run.id);
+    if (mine)
+        for_pages(a.ref_counts, run.lo, run.hi, [&](int64_t b, uint32_t c) {
+            const uint32_t freed = __ballot_sync(0xFFFFFFFFu, c == kFreedMark);
+            const uint32_t to = at + __popc(freed & below);
+            if (c == kFreedMark) {
+                a.ref_counts[b] = 0;
+                if (to < a.num_blocks) a.free_blocks[to] = (uint32_t)b;
+                else flag_error(a.status, kDevBadBlock);      // more free pages than the pool has
+            }
+            at += __popc(freed);
+        });
+    if (run.id == 0) {
+        const uint32_t total = count_before(counts, kRuns);
+        if (threadIdx.x == 0) *a.num_free = (uint32_t)min((int64_t)top + total, a.num_blocks);
     }
-    cl.sync();                                           // every CTA has read the top
-    if (cl.block_rank() == 0 && threadIdx.x == 0) *a.num_free = (uint32_t)min((int64_t)top + total, a.num_blocks);
 }
 
 // ---- compact: with L pages held, the k-th held page >= L moves to the k-th
 // free page < L.  remap[b] for every b >= L: where it went, or b itself.
+//
+// Below L a run's first free page has rank lo - (pages held before the run);
+// above L its first held page has rank (held before the run) - (held below L),
+// and the last term needs a count of only the run that L falls into, which
+// every warp makes for itself.
 __global__ void __cluster_dims__(kCluster) __launch_bounds__(kPlanThreads)
 compact_plan_kernel(PoolArgs a, uint32_t *move_src, uint32_t *move_dst, int64_t capacity, uint32_t *remap) {
     cg::cluster_group cl = cg::this_cluster();
-    int64_t lo, hi;
-    share_of(a.num_blocks, cl.block_rank(), lo, hi);
-    uint32_t n = 0;
-    for (int64_t b = lo + threadIdx.x; b < hi; b += kPlanThreads) n += a.ref_counts[b] != 0;
-    unsigned long long mine;
-    scan_cta(n, mine);
-    uint32_t live;
-    scan_cluster(cl, (uint32_t)mine, live);
-    uint32_t holes = 0, movers = 0;
-    for (int64_t b = lo + threadIdx.x; b < hi; b += kPlanThreads) {
-        const bool used = a.ref_counts[b] != 0;
-        holes += !used && b < live;
-        movers += used && b >= live;
-    }
-    unsigned long long both;
-    scan_cta((unsigned long long)holes << 32 | movers, both);
-    uint32_t moves, same;
-    uint32_t at_hole = scan_cluster(cl, (uint32_t)(both >> 32), moves);
-    uint32_t at_mover = scan_cluster(cl, (uint32_t)both, same);
-    for (int64_t b0 = lo; b0 < hi; b0 += kPlanThreads) {
-        const int64_t b = b0 + threadIdx.x;
-        const bool in = b < hi;
-        const bool used = in && a.ref_counts[b] != 0;
-        const bool hole = in && !used && b < live, mover = used && b >= live;
-        unsigned long long here;
-        const unsigned long long k = scan_cta((unsigned long long)hole << 32 | (mover ? 1u : 0u), here);
-        if (hole) move_dst[at_hole + (uint32_t)(k >> 32)] = (uint32_t)b;
-        if (mover) move_src[at_mover + (uint32_t)k] = (uint32_t)b;
-        if (in && b >= live) remap[b] = (uint32_t)b;
-        at_hole += (uint32_t)(here >> 32);
-        at_mover += (uint32_t)here;
-    }
+    cl.barrier_arrive();
+    const Run run = run_of(cl, a.num_blocks);
+    const uint32_t below = (1u << (threadIdx.x & 31)) - 1;
+    __shared__ uint32_t counts[kRuns];
+    uint32_t mine = 0;
+    for_pages(a.ref_counts, run.lo, run.hi, [&](int64_t, uint32_t c) {
+        mine += __popc(__ballot_sync(0xFFFFFFFFu, c != 0));
+    });
+    share_count(cl, counts, run.id, mine);
+    const uint32_t live = count_before(counts, kRuns), held_before = count_before(counts, run.id);
+    const int split = (int)(live / run.per);             // run.per >= 32; kRuns when the pool is full
+    uint32_t held_below = count_before(counts, split);
+    for_pages(a.ref_counts, min(a.num_blocks, run.per * split), (int64_t)live, [&](int64_t, uint32_t c) {
+        held_below += __popc(__ballot_sync(0xFFFFFFFFu, c != 0));
+    });
+    const uint32_t moves = live - held_below;
+    uint32_t at_hole = (uint32_t)run.lo - held_before, at_mover = max(held_before, held_below) - held_below;
+    for_pages(a.ref_counts, run.lo, run.hi, [&](int64_t b, uint32_t c) {
+        const bool hole = c == 0 && b < min((int64_t)live, run.hi), mover = c != 0 && b >= live;
+        const uint32_t holes = __ballot_sync(0xFFFFFFFFu, hole), movers = __ballot_sync(0xFFFFFFFFu, mover);
+        if (hole) move_dst[at_hole + __popc(holes & below)] = (uint32_t)b;
+        if (mover) move_src[at_mover + __popc(movers & below)] = (uint32_t)b;
+        if (b >= live && b < run.hi) remap[b] = (uint32_t)b;
+        at_hole += __popc(holes);
+        at_mover += __popc(movers);
+    });
     cl.sync();                                           // both lists and remap stand
     const int64_t step = (int64_t)kCluster * kPlanThreads;
     for (int64_t k = (int64_t)cl.block_rank() * kPlanThreads + threadIdx.x; k < max(capacity, a.num_blocks); k += step) {
