@@ -107,6 +107,7 @@ struct Plan {                          // in the workspace
 struct Geometry {
     int group;                         // query heads of a kv head
     int heads;                         // of them in one tile: min(group, 128)
+    uint32_t over_heads;               // ceil(2^16 / heads): row / heads == row * over_heads >> 16 for rows < 128
     int tokens;                        // tokens in a row tile: 128 / heads
     int span;                          // tokens of an item: NT * tokens
     int groups;                        // CTAs per (row tile, K/V piece): kv heads x head slices
@@ -436,11 +437,11 @@ __device__ __forceinline__ void load_row(const T *p, float (&x)[N]) {
     }
 }
 
+// 16 bytes of a row of T.
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float *x) {
+__device__ __forceinline__ uint4 chunk_of(const float *x) {
     if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -452,7 +453,7 @@ __device__ __forceinline__ void store8(T *p, const float *x) {
                 w[k] = *reinterpret_cast<const uint32_t *>(&v);
             }
         }
-        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -551,51 +552,66 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     const int head0 = slice * P.g.heads;                                 // first head of the kv head's group
     const int heads = min(P.g.heads, P.g.group - head0);
 
-    // ---- Q: a warp per row; f16 parts of q 2^-e into the swizzled tiles
+    // ---- Q: f16 parts of q 2^-e into the swizzled tiles.  Each lane has two
+    // runs of 8 elements of a row, so D / 16 lanes share one and a warp has
+    // several in hand; all its loads are under way before the first is used.
+    // (A warp per row, loads behind a branch per row: 8600 cycles an item, not 4600.)
     if (tiles > 0) {
-        constexpr int PER = D / 32;
+        constexpr int LPR = D / 16, RPW = 32 / LPR;          // lanes of a row, rows of a warp at once
         constexpr int WARPS = C::THREADS / 32;
-        constexpr int BATCH = D == 256 ? 6 : 8;              // rows in flight per warp
-        for (int r0 = warp; r0 < C::ROWS; r0 += WARPS * BATCH) {
-            float x[BATCH][PER];
+        constexpr int ROUNDS = (C::ROWS + WARPS * RPW - 1) / (WARPS * RPW);
+        constexpr int BATCH = ROUNDS > 4 ? (ROUNDS + 1) / 2 : ROUNDS;
+        const int l = lane % LPR;
+#pragma unroll 1
+        for (int u0 = 0; u0 < ROUNDS; u0 += BATCH) {
+            alignas(16) T q[BATCH][16];
+            bool have[BATCH];
 #pragma unroll
             for (int u = 0; u < BATCH; ++u) {
-                const int r = r0 + u * WARPS;
-                const int rt = r & 127, tok = rt / P.g.heads, h = rt % P.g.heads;
+                const int r = ((u0 + u) * WARPS + warp) * RPW + lane / LPR;
+                const int rt = r & 127, tok = (int)(rt * P.g.over_heads >> 16), h = rt - tok * P.g.heads;
                 const uint32_t i = e.y * P.g.span + (r >> 7) * P.g.tokens + tok;
-                if (r < C::ROWS && tok < P.g.tokens && h < heads && i < n) {
-                    load_row(static_cast<const T *>(a.q) + (int64_t)(row0 + i) * a.q_stride +
-                                 (int64_t)(kvh * P.g.group + head0 + h) * D + lane * PER, x[u]);
-                } else {
+                have[u] = r < C::ROWS && tok < P.g.tokens && h < heads && i < n;
+                // rows that do not exist: loaded from the first one that does, and made zeros
+                const T *p = static_cast<const T *>(a.q) + (int64_t)(row0 + (have[u] ? i : 0u)) * a.q_stride +
+                             (int64_t)(kvh * P.g.group + head0 + (have[u] ? h : 0)) * D + 8 * l;
+                constexpr int V = 8 * sizeof(T) / 16;
 #pragma unroll
-                    for (int k = 0; k < PER; ++k) x[u][k] = 0.0f;
-                }
+                for (int c = 0; c < 2 * V; ++c)
+                    reinterpret_cast<uint4 *>(q[u])[c] =
+                        __ldg(reinterpret_cast<const uint4 *>(p + c / V * (D / 2)) + c % V);
             }
 #pragma unroll
             for (int u = 0; u < BATCH; ++u) {
-                const int r = r0 + u * WARPS, rt = r & 127;
-                if (r >= C::ROWS) break;
-                float mx = 0.0f;
+                const int r = ((u0 + u) * WARPS + warp) * RPW + lane / LPR, rt = r & 127;
+                float x[2][8], mx = 0.0f;
+                load_row(q[u], x[0]);
+                load_row(q[u] + 8, x[1]);
 #pragma unroll
-                for (int k = 0; k < PER; ++k) mx = fmaxf(mx, fabsf(x[u][k]));
-                mx = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(mx)));
+                for (int k = 0; k < 16; ++k) x[k / 8][k % 8] = have[u] ? x[k / 8][k % 8] : 0.0f;
+#pragma unroll
+                for (int k = 0; k < 16; k += 2) mx = max3f(mx, fabsf(x[k / 8][k % 8]), fabsf(x[k / 8][k % 8 + 1]));
+#pragma unroll
+                for (int d = 1; d < LPR; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                if (r >= C::ROWS) continue;
                 const int eq = mx > 0.0f ? max(-126, min(126, (int)(__float_as_uint(mx) >> 23) - 127)) : 0;
                 const float down = __uint_as_float((uint32_t)(127 - eq) << 23);
-                if (lane == 0)
+                if (l == 0)
                     reinterpret_cast<float *>(smem + C::QF_OFF)[r] = __uint_as_float((uint32_t)(127 + eq) << 23);
-                uint32_t hi[PER / 2], lo[PER / 2];
 #pragma unroll
-                for (int k = 0; k < PER / 2; ++k) {
-                    if (NP == 2) split_f16x2(x[u][2 * k] * down, x[u][2 * k + 1] * down, hi[k], lo[k]);
-                    else hi[k] = pack_f16x2(x[u][2 * k] * down, x[u][2 * k + 1] * down);
-                }
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t hi[4];
+                    [[maybe_unused]] uint32_t lo[4];
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    uint8_t *dst = smem + C::Q_OFF + ((r >> 7) * NP + p) * C::Q_PART + swz(rt, lane * PER, 128);
-                    const uint32_t *v = p ? lo : hi;
-                    if constexpr (PER == 2) *reinterpret_cast<uint32_t *>(dst) = v[0];
-                    else if constexpr (PER == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(v[0], v[1]);
-                    else *reinterpret_cast<uint4 *>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int k = 0; k < 4; ++k) {
+                        const float y0 = x[c][2 * k] * down, y1 = x[c][2 * k + 1] * down;
+                        if constexpr (NP == 2) split_f16x2(y0, y1, hi[k], lo[k]);
+                        else hi[k] = pack_f16x2(y0, y1);
+                    }
+                    uint8_t *dst = smem + C::Q_OFF + (r >> 7) * NP * C::Q_PART + swz(rt, 8 * l + c * (D / 2), 128);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if constexpr (NP == 2)
+                        *reinterpret_cast<uint4 *>(dst + C::Q_PART) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
         }
@@ -634,7 +650,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
 
     if (warp >= 4 * NS + 4) {
         // -------------------------------------------------- issue and tables
-        set_regs_down<80>();
+        set_regs_down<NS == 2 ? 80 : 96>();
         // descriptors of the first tiles; offsets within and between tiles add to them in 16-byte units
         auto step_of = [](int job) { return C::MODE == kPair ? job >> 1 : job; };
         if (warp == 4 * NS + 4 && elect_one()) {
@@ -830,12 +846,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         }
     } else {
         // ---------------------------------------------------------- softmax
-        // 2 x 160 + 112 + 80 = 4 x 128 registers a thread at launch; Single: 208 + 168 + 80 <= 3 x 168
+        // 2 x 160 + 112 + 80 = 4 x 128 registers a thread at launch; Single: 208 + 168 + 96 <= 3 x 168
         set_regs_up<NS == 2 ? 160 : 208>();
         const int wg = warp >> 2;                            // accumulator
         const int rt = tid & 127;                            // row of the tile
         const int nt = C::MODE == kPair ? wg : 0;
-        const int tok = rt / P.g.heads, h = rt % P.g.heads;
+        const int tok = (int)(rt * P.g.over_heads >> 16), h = rt - tok * P.g.heads;
         const uint32_t i = e.y * P.g.span + nt * P.g.tokens + tok;
         const bool row_ok = tok < P.g.tokens && h < heads && i < n;
         // rows that do not exist are computed as if they saw everything, and not stored
@@ -1050,36 +1066,86 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 rec[D] = R;
                 rec[D + 1] = l;
             }
-            const int k_lo = C::MODE == kSplit ? wg * (D / 2) : 0, k_hi = C::MODE == kSplit ? k_lo + D / 2 : D;
-#pragma unroll 1
-            for (int k = k_lo; k < k_hi; k += 16) {
-                float o[16];
+            // 32 columns of accumulator x
+            auto gather = [&](int x, float g, int k, float (&o)[32]) {
+                tmem_ld32((C::MODE == kSplit ? tO + x * D + lanes : tOw) + k, o);
+                if constexpr (NP == 2) {
+                    if (!flushes(x)) return;
+                    const float4 *at = reinterpret_cast<const float4 *>(sums_of(x) + k);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const float4 v = at[y];
+                        o[4 * y] = fmaf(v.x, g, o[4 * y]);
+                        o[4 * y + 1] = fmaf(v.y, g, o[4 * y + 1]);
+                        o[4 * y + 2] = fmaf(v.z, g, o[4 * y + 2]);
+                        o[4 * y + 3] = fmaf(v.w, g, o[4 * y + 3]);
+                    }
+                }
+            };
+            // 32 columns of the row (a row without weights has zeros, whatever its accumulator
+            // holds; selected where that costs the kernel at hand no spilled registers)
+            auto columns = [&](int k, float (&o)[32]) {
+                const bool none = tiles <= 0 || l == 0.0f;
                 if (tiles > 0) {
-                    const float *s0 = flushes(0) ? sums_of(C::MODE == kPair ? wg : 0) + k : nullptr;
-                    tmem_ld16(C::MODE == kSplit ? tO + lanes + k : tOw + k, o);
+                    gather(C::MODE == kPair ? wg : 0, g0, k, o);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        o[x] = l == 0.0f ? 0.0f : (flushes(C::MODE == kPair ? wg : 0) ? fmaf(s0[x], g0, o[x]) : o[x]) * f0;
+                    for (int x = 0; x < 32; ++x) o[x] = NP == 1 && none ? 0.0f : o[x] * f0;
                     if (both) {
-                        const float *s1 = flushes(1) ? sums_of(1) + k : nullptr;
-                        float o1[16];
-                        tmem_ld16(tO + D + lanes + k, o1);
+                        float o1[32];
+                        gather(1, g1, k, o1);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            o[x] += l == 0.0f ? 0.0f : (flushes(1) ? fmaf(s1[x], g1, o1[x]) : o1[x]) * f1;
-                    }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) o[x] = 0.0f;
-                }
-                if (row_ok) {
-#pragma unroll
-                    for (int x = 0; x < 16; x += 8) {
-                        if (piece) store8(rec + k + x, o + x);
-                        else store8(dst + k + x, o + x);
+                        for (int x = 0; x < 32; ++x) o[x] = fmaf(o1[x], f1, o[x]);
                     }
                 }
-            }
+                if (NP == 1 ? tiles <= 0 || (both && none) : none) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) o[x] = 0.0f;
+                }
+            };
+            // Through shared memory, so that each store writes whole lines: up to
+            // 128 bytes a row at a time.  The place is the row tile's Q (its last
+            // QK is done; Split: and what follows it, since all MMAs are).
+            // (Rows written by their threads: 5700 cycles an item, not 3000; f32 10,100, not 3900.)
+            auto write = [&](auto *row) {
+                using O = std::remove_pointer_t<decltype(row)>;
+                constexpr int COLS = C::MODE == kSplit ? D / 2 : D;
+                constexpr int CH = COLS * sizeof(O) < 128 ? COLS * sizeof(O) / 16 : 8;   // 16-byte chunks of a row
+                constexpr int STEP = CH * 16 / sizeof(O);                                // columns
+                const int k_lo = C::MODE == kSplit ? wg * COLS : 0;
+                uint8_t *buf = smem + C::Q_OFF + (C::MODE == kPair ? nt * C::Q_PART : 0) +
+                               (C::MODE == kSplit ? warp : warp & 3) * (32 * 16 * CH);
+                auto chunk_at = [&](int r, int c) { return buf + r * (16 * CH) + ((c ^ (r / (8 / CH))) & (CH - 1)) * 16; };
+                const uint32_t exist = __ballot_sync(0xFFFFFFFFu, row_ok);
+                O *rows[CH];                                  // the rows that this lane writes a chunk of
+#pragma unroll
+                for (int x = 0; x < CH; ++x)
+                    rows[x] = reinterpret_cast<O *>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row),
+                                                                x * (32 / CH) + lane / CH)) +
+                              lane % CH * (16 / (int)sizeof(O));
+#pragma unroll 1
+                for (int k = k_lo; k < k_lo + COLS; k += STEP) {
+#pragma unroll
+                    for (int k0 = 0; k0 < STEP; k0 += 32) {
+                        float o[32];
+                        columns(k + k0, o);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 16 / sizeof(O)) {
+                            const uint4 v = chunk_of<O>(o + x);
+                            *reinterpret_cast<uint4 *>(chunk_at(lane, (k0 + x) * (int)sizeof(O) / 16)) = v;
+                        }
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int x = 0; x < CH; ++x) {
+                        const int r = x * (32 / CH) + lane / CH;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(chunk_at(r, lane % CH));
+                        if (exist >> r & 1u) *reinterpret_cast<uint4 *>(rows[x] + k) = v;
+                    }
+                    __syncwarp();
+                }
+            };
+            if (piece) write(rec);
+            else write(dst);
         }
     }
     tc_fence_before();
@@ -1174,6 +1240,7 @@ size_t layout(const PrefillArgs &a, Params &P) {
     g.group = a.num_heads / a.num_kv_heads;
     g.heads = g.group < 128 ? g.group : 128;
     g.slices = (g.group + 127) / 128;
+    g.over_heads = (65536u + g.heads - 1) / g.heads;
     g.tokens = 128 / g.heads;
     g.span = nt * g.tokens;
     g.groups = a.num_kv_heads * g.slices;
