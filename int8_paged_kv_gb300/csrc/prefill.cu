@@ -22,6 +22,7 @@
 //
 // Masks.  A token that a row does not see has p = 0 by selection, whatever its
 // words hold, and does not enter the row's reference.
+#include <algorithm>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -94,10 +95,11 @@ struct Item {
 };
 
 struct Plan {                          // in the workspace
-    uint32_t *head;                    // entries, items, K/V tiles per entry
+    uint32_t *head;                    // entries, items, K/V tiles that pay for a piece, split items
     uint32_t *first;                   // [num_seqs + 1] items before a sequence's first
     uint4 *entries;                    // [cap_entries], most K/V tiles first
-    uint4 *items;                      // [cap_items]: seq, tile, first slot, pieces
+    uint4 *items;                      // [cap_items]: seq, tile, K/V tiles, first slot
+    uint4 *splits;                     // [cap_slots]: of the items in pieces: seq, tile, first slot, pieces
     float *part;                       // [slots][groups][ROWS][D + 4]
     float *sums;                       // [SMs][accumulators][128][D], or none
     uint32_t *places;                  // a bit per place in sums: taken
@@ -123,10 +125,38 @@ struct Params {
     int rows;                          // rows of an item (128 NT)
     int tn;                            // context tokens per K/V tile
     int may_split;
+    int fine;                          // there is room for fine pieces
 };
 
+// Items are cut into pieces, each with a CTA and a record of its own, when there
+// are too few of them to keep the SMs equally busy.  With p = (K/V tiles of all)
+// / SMs: coarsely, an item longer than 2 p into pieces of about p, so that few
+// items fill one wave; or finely, into pieces of about p / kFine, which even out
+// between the SMs however the items divide.  A piece costs the time of kCost
+// tiles; the way that should end first is taken.  (Two prompts of 512 rows behind
+// 130,000 and 60,000 tokens, 256 CTAs: 2634 us uncut, 1913 finely; 128 equal CTAs
+// of 8192 tokens: 196 us uncut, 270 finely.)
 constexpr int kWave = 152;             // SMs of a GB300: CTAs at a time
 constexpr int kMinPiece = 512;         // context tokens that pay for a piece of their own
+constexpr int kFine = 8;
+constexpr float kCost = 2.0f;          // 10,000 cycles
+constexpr int kMaySplit = 4 * kWave;   // CTAs without pieces above which nothing is cut
+
+// Whether fine pieces can pay: ctas items of `longest` tiles at most, `share` tiles per SM,
+// the shorter half of them `low` long on average.
+__device__ inline bool fine_pays(float ctas, float longest, float share, float low, float min_piece) {
+    const float fine = fmaxf(share / kFine, min_piece);
+    const float coarse = ctas <= kWave ? fminf(longest, share * (1.0f + ctas / kWave))
+                                       : fmaxf(fminf(longest, 1.5f * share), share + 0.5f * low);
+    return share * (1.0f + kCost / fine) + 0.5f * fine < coarse;
+}
+
+// Pieces of an item of this many K/V tiles, and their length but the last's.
+__device__ __forceinline__ uint32_t pieces_of(uint32_t tiles, uint32_t piece, uint32_t &len) {
+    const uint32_t n = max(1u, tiles / piece);
+    len = max(1u, (tiles + n - 1) / n);
+    return tiles ? (tiles + len - 1) / len : 1u;
+}
 
 __device__ __forceinline__ uint32_t context_of(const PrefillArgs &a, uint32_t s) {
     return (uint32_t)min((int64_t)a.context_lens[s], (int64_t)a.max_blocks_per_seq * a.block_size);
@@ -182,13 +212,17 @@ __device__ uint32_t scan_plan(uint32_t x, uint32_t &total) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
     __shared__ uint32_t bucket[kBuckets];
-    __shared__ unsigned long long sum_tiles;
+    __shared__ unsigned long long sum_tiles, low_tiles;
+    __shared__ uint32_t longest, low_items;
     grid_dependents_launch();
     const PrefillArgs &a = P.a;
     const int tid = threadIdx.x;
     bucket[tid] = 0;
     if (tid < (a.num_sms + 31) / 32) P.plan.places[tid] = 0;
-    if (tid == 0) sum_tiles = 0;
+    if (tid == 0) {
+        sum_tiles = low_tiles = 0;
+        longest = low_items = 0;
+    }
     uint32_t items = 0, bound = 0;                       // bound: the largest start so far
     for (int s0 = 0; s0 < a.num_seqs; s0 += kPlanThreads) {
         const int s = s0 + tid;
@@ -223,36 +257,61 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
         const uint32_t n = rows_of(a, s, row0);
         return (uint32_t)((most_seen(context_of(a, s), n, tile * P.g.span, P.g.span) + P.tn - 1) / P.tn);
     };
-    uint32_t piece = 0x7FFFFFFFu;                        // K/V tiles of an entry at most
+    uint32_t piece = 0x7FFFFFFFu;
     const uint32_t ctas = items * P.g.groups;
-    if (P.may_split && ctas < 2 * kWave * 3 / 4) {
-        unsigned long long mine = 0;
+    if (P.may_split && ctas < kMaySplit) {
+        // each thread keeps to its items, so it may read what it wrote
+        unsigned long long sum = 0;
+        uint32_t top = 0;
         for (uint32_t i = tid; i < items; i += kPlanThreads) {
             uint32_t s, tile;
-            mine += item_of(i, s, tile);
+            const uint32_t tiles = item_of(i, s, tile);
+            P.plan.items[i] = make_uint4(s, tile, tiles, 0u);
+            sum += tiles;
+            top = max(top, tiles);
         }
-        if (mine) atomicAdd(&sum_tiles, mine);
+        if (sum) {
+            atomicAdd(&sum_tiles, sum);
+            atomicMax(&longest, top);
+        }
         __syncthreads();
-        // pieces of equal size in one wave of CTAs, or in two when one is nearly full
-        const uint32_t room = (ctas < kWave * 3 / 4 ? kWave : 2 * kWave) - ctas;
-        piece = max((uint32_t)(kMinPiece / P.tn),
-                    (uint32_t)((sum_tiles * P.g.groups + room - 1) / max(room, 1u)));
+        uint32_t low = 0, lows = 0;                          // items up to the mean
+        for (uint32_t i = tid; i < items; i += kPlanThreads) {
+            const uint32_t tiles = P.plan.items[i].z;
+            if ((unsigned long long)tiles * items <= sum_tiles) {
+                low += tiles;
+                ++lows;
+            }
+        }
+        if (lows) {
+            atomicAdd(&low_tiles, (unsigned long long)low);
+            atomicAdd(&low_items, lows);
+        }
+        __syncthreads();
+        const unsigned long long all = sum_tiles * P.g.groups;
+        const int waves = P.fine && fine_pays((float)ctas, (float)longest, (float)all / kWave,
+                                    (float)low_tiles / (float)max(low_items, 1u), (float)(kMinPiece / P.tn)) ? kFine : 1;
+        piece = max((uint32_t)(kMinPiece / P.tn), (uint32_t)((all + kWave * waves - 1) / (kWave * waves)));
     }
-    uint32_t slots = 0;
+    uint32_t slots = 0, splits = 0;
     for (uint32_t i0 = 0; i0 < items; i0 += kPlanThreads) {
         const uint32_t i = i0 + tid;
         uint32_t s = 0, tile = 0, tiles = 0, np = 0;
         if (i < items) {
+            uint32_t len;
             tiles = item_of(i, s, tile);
-            np = max(1u, (tiles + piece - 1) / piece);
+            np = pieces_of(tiles, piece, len);
             for (uint32_t p = 0; p < np; ++p)
-                atomicAdd(&bucket[kBuckets - 1 - min(min(tiles - p * piece, piece), (uint32_t)kBuckets - 1)], 1u);
+                atomicAdd(&bucket[kBuckets - 1 - min(min(tiles - p * len, len), (uint32_t)kBuckets - 1)], 1u);
         }
         if (P.may_split) {
-            uint32_t total;
+            uint32_t total, count;
             const uint32_t at = slots + scan_plan(np > 1 ? np : 0u, total);
-            if (i < items) P.plan.items[i] = make_uint4(s, tile, at, np);
+            const uint32_t k = splits + scan_plan(np > 1 ? 1u : 0u, count);
+            if (i < items) P.plan.items[i].w = at;
+            if (np > 1 && k < P.plan.cap_slots) P.plan.splits[k] = make_uint4(s, tile, at, np);
             slots += total;
+            splits += count;
         }
     }
     __syncthreads();
@@ -263,19 +322,21 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
     for (uint32_t i = tid; i < items; i += kPlanThreads) {
         uint32_t s, tile;
         const uint32_t tiles = item_of(i, s, tile);
-        const uint32_t np = max(1u, (tiles + piece - 1) / piece);
-        const uint32_t slot = P.may_split ? P.plan.items[i].z : 0u;
+        uint32_t len;
+        const uint32_t np = pieces_of(tiles, piece, len);
+        const uint32_t slot = P.may_split ? P.plan.items[i].w : 0u;
         for (uint32_t p = 0; p < np; ++p) {
             const uint32_t at =
-                atomicAdd(&bucket[kBuckets - 1 - min(min(tiles - p * piece, piece), (uint32_t)kBuckets - 1)], 1u);
+                atomicAdd(&bucket[kBuckets - 1 - min(min(tiles - p * len, len), (uint32_t)kBuckets - 1)], 1u);
             if (at < P.plan.cap_entries)
-                P.plan.entries[at] = make_uint4(s, tile, p * piece, np > 1 ? slot + p : 0xFFFFFFFFu);
+                P.plan.entries[at] = make_uint4(s, tile, p * len, np > 1 ? slot + p : 0xFFFFFFFFu);
         }
     }
     if (tid == 0) {
         P.plan.head[0] = (uint32_t)min((int64_t)entries, P.plan.cap_entries);
         P.plan.head[1] = items;
         P.plan.head[2] = piece;
+        P.plan.head[3] = splits;
     }
 }
 
@@ -505,7 +566,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     volatile uint32_t *tmem_at = reinterpret_cast<volatile uint32_t *>(smem + C::BAR_OFF + C::BARS * 8);
     volatile uint32_t *abort = tmem_at + 1, *place = tmem_at + 2;
 
-    // set up while the planning kernel ends
+    // the grid is the plan's upper bound
+    const uint32_t entry = blockIdx.x / P.g.groups, cta = blockIdx.x % P.g.groups;
+    if (P.may_split && blockIdx.x >= kWave) {
+        grid_dependency_wait();
+        if (entry >= P.plan.head[0]) return;
+    }
+    // the first wave: set up while the planning kernel ends
     if (warp == 0) tmem_alloc(s0 + C::BAR_OFF + C::BARS * 8, 512);
     if (tid == 32) {
         for (int i = 0; i < C::BARS; ++i) {
@@ -520,8 +587,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     grid_dependency_wait();
 
     const PrefillArgs &a = P.a;
-    const uint32_t entry = blockIdx.x / P.g.groups, cta = blockIdx.x % P.g.groups;
-    if (entry >= P.plan.head[0]) {                       // the grid is the plan's upper bound
+    if (entry >= P.plan.head[0]) {
         __syncthreads();
         if (warp == 0) tmem_dealloc(*tmem_at, 512);
         return;
@@ -532,7 +598,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     const uint32_t n = rows_of(a, e.x, row0), c = context_of(a, e.x);
     const int seen_all = most_seen(c, n, e.y * P.g.span, P.g.span);
     const int j0 = (int)e.z;
-    const int tiles = min((seen_all + CT - 1) / CT - j0, (int)P.plan.head[2]);
+    uint32_t piece_len;
+    pieces_of((uint32_t)(seen_all + CT - 1) / CT, P.plan.head[2], piece_len);
+    const int tiles = min((seen_all + CT - 1) / CT - j0, (int)piece_len);
     const int steps = min(tiles * SUB, (seen_all + TN - 1) / TN - j0 * SUB);     // of TN tokens
     const int jobs = C::MODE == kPair ? 2 * steps : steps;
     // whether accumulator x is flushed before the end
@@ -1172,52 +1240,58 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
 //
 // A warp per row of a split item: the pieces' records, weighted by their
 // references.  Pieces in order, so the sum does not depend on the schedule.
+// Bound by the records, D + 4 floats a row and piece, read once.
+constexpr int kJoinPerSm = 8;
+
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kernel(Params P) {
     grid_dependency_wait();
-    const uint32_t item = blockIdx.x / P.g.groups, cta = blockIdx.x % P.g.groups;
-    if (item >= P.plan.head[1]) return;
-    const uint4 it = P.plan.items[item];
-    if (it.w < 2) return;
     const PrefillArgs &a = P.a;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int rt = r & 127, tok = rt / P.g.heads, h = rt % P.g.heads;
-    const int kvh = cta / P.g.slices, head0 = (cta % P.g.slices) * P.g.heads;
-    uint32_t row0;
-    const uint32_t n = rows_of(a, it.x, row0);
-    const uint32_t i = it.y * P.g.span + (r >> 7) * P.g.tokens + tok;
-    if (tok >= P.g.tokens || h >= min(P.g.heads, P.g.group - head0) || i >= n) return;
-    constexpr int PER = D / 32;
-    const int64_t step = (int64_t)P.g.groups * P.rows * (D + 4);
-    const float *rec = P.plan.part + (((int64_t)it.z * P.g.groups + cta) * P.rows + r) * (D + 4);
-    float Rm = -INFINITY;
-    for (uint32_t p = lane; p < it.w; p += 32) Rm = fmaxf(Rm, rec[p * step + D]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t per = P.rows / 8;                         // CTAs of one piece's rows
+    const uint64_t units = (uint64_t)P.plan.head[3] * P.g.groups * per;
+    for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int r = (int)(u % per) * 8 + warp;
+        const uint32_t cta = (uint32_t)(u / per) % P.g.groups;
+        const uint4 it = P.plan.splits[u / per / P.g.groups];
+        const int rt = r & 127, tok = (int)(rt * P.g.over_heads >> 16), h = rt - tok * P.g.heads;
+        const int kvh = cta / P.g.slices, head0 = (cta % P.g.slices) * P.g.heads;
+        uint32_t row0;
+        const uint32_t n = rows_of(a, it.x, row0);
+        const uint32_t i = it.y * P.g.span + (r >> 7) * P.g.tokens + tok;
+        if (tok >= P.g.tokens || h >= min(P.g.heads, P.g.group - head0) || i >= n) continue;
+        constexpr int PER = D / 32;
+        const int64_t step = (int64_t)P.g.groups * P.rows * (D + 4);
+        const float *rec = P.plan.part + (((int64_t)it.z * P.g.groups + cta) * P.rows + r) * (D + 4);
+        float Rm = -INFINITY;
+        for (uint32_t p = lane; p < it.w; p += 32) Rm = fmaxf(Rm, rec[p * step + D]);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) Rm = fmaxf(Rm, __shfl_xor_sync(0xFFFFFFFFu, Rm, d));
-    float l = 0.0f, o[PER];
+        for (int d = 16; d; d >>= 1) Rm = fmaxf(Rm, __shfl_xor_sync(0xFFFFFFFFu, Rm, d));
+        float l = 0.0f, o[PER];
 #pragma unroll
-    for (int k = 0; k < PER; ++k) o[k] = 0.0f;
+        for (int k = 0; k < PER; ++k) o[k] = 0.0f;
 #pragma unroll 4
-    for (uint32_t p = 0; p < it.w; ++p) {
-        const float *x = rec + p * step;
-        const float R = x[D], lp = x[D + 1];
-        float v[PER];
-        load_row(x + lane * PER, v);
-        if (lp == 0.0f) continue;                            // the piece has no token that the row sees
-        const float f = R == -INFINITY ? 1.0f : fast_exp2(R - Rm);
-        l += f * lp;
+        for (uint32_t p = 0; p < it.w; ++p) {
+            const float *x = rec + p * step;
+            const float R = x[D], lp = x[D + 1];
+            float v[PER];
+            load_row(x + lane * PER, v);
+            if (lp == 0.0f) continue;                        // the piece has no token that the row sees
+            const float f = R == -INFINITY ? 1.0f : fast_exp2(R - Rm);
+            l += f * lp;
 #pragma unroll
-        for (int k = 0; k < PER; ++k) o[k] += f * v[k];
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    T *dst = static_cast<T *>(a.out) + (int64_t)(row0 + i) * a.out_stride +
-             (int64_t)(kvh * P.g.group + head0 + h) * D + lane * PER;
+            for (int k = 0; k < PER; ++k) o[k] += f * v[k];
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        T *dst = static_cast<T *>(a.out) + (int64_t)(row0 + i) * a.out_stride +
+                 (int64_t)(kvh * P.g.group + head0 + h) * D + lane * PER;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const float y = o[k] * inv;
-        if constexpr (sizeof(T) == 4) dst[k] = y;
-        else if constexpr (std::is_same<T, __half>::value) dst[k] = __float2half_rn(y);
-        else dst[k] = __float2bfloat16_rn(y);
+        for (int k = 0; k < PER; ++k) {
+            const float y = o[k] * inv;
+            if constexpr (sizeof(T) == 4) dst[k] = y;
+            else if constexpr (std::is_same<T, __half>::value) dst[k] = __float2half_rn(y);
+            else dst[k] = __float2bfloat16_rn(y);
+        }
     }
 }
 
@@ -1248,11 +1322,19 @@ size_t layout(const PrefillArgs &a, Params &P) {
     P.tn = a.head_size == 256 ? kTN : 2 * kTN;           // tokens of a K/V tile: items are cut between tiles
     const int64_t least = (a.num_rows + g.span - 1) / g.span;        // items, at least and at most
     const int64_t most = a.num_rows / g.span + (a.num_seqs < a.num_rows ? a.num_seqs : a.num_rows);
-    P.may_split = least * g.groups < 2 * kWave * 3 / 4 &&
-                  (int64_t)a.max_blocks_per_seq * a.block_size > kMinPiece;
+    const int64_t room = (int64_t)a.max_blocks_per_seq * a.block_size;
     Plan &p = P.plan;
     p.cap_items = most;
-    p.cap_slots = P.may_split ? 2 * kWave / g.groups + 1 : 0;        // pieces of split items
+    // Whether fine pieces can pay at all (fine_pays, solved for the largest share that the room
+    // allows).  Where they cannot, no place is kept for them: every 152 CTAs that the grid has
+    // too many of cost 1 us.
+    const double ctas = (double)(most * g.groups), part = ctas / kWave, share = part * ((room + P.tn - 1) / P.tn);
+    P.fine = least * g.groups < kMaySplit && room >= 2 * kMinPiece &&
+             (part > 1.0 ? share > 36.0 : share * (part - 0.0625) > 16.0 || share * (part - 0.5) > 2.0);
+    P.may_split = P.fine || (least * g.groups < kWave && room >= 2 * kMinPiece);
+    const int64_t waves = P.fine ? kFine : 1;
+    // pieces of split items: tiles / piece of each, at most
+    p.cap_slots = P.may_split ? std::min<int64_t>(kWave * waves / g.groups + 1, most * ((room + P.tn) / kMinPiece)) : 0;
     p.cap_entries = most + p.cap_slots;
     char *base = static_cast<char *>(a.workspace);
     size_t at = 0;
@@ -1265,6 +1347,7 @@ size_t layout(const PrefillArgs &a, Params &P) {
     p.first = reinterpret_cast<uint32_t *>(take((size_t)(a.num_seqs + 1) * 4));
     p.entries = reinterpret_cast<uint4 *>(take((size_t)p.cap_entries * 16));
     p.items = reinterpret_cast<uint4 *>(take(P.may_split ? (size_t)p.cap_items * 16 : 0));
+    p.splits = reinterpret_cast<uint4 *>(take((size_t)p.cap_slots * 16));
     p.part = reinterpret_cast<float *>(take((size_t)p.cap_slots * g.groups * P.rows * (a.head_size + 4) * 4));
     p.places = reinterpret_cast<uint32_t *>(take((size_t)(a.num_sms + 31) / 32 * 4));
     // (a context short of the shortest flush needs no sums)
@@ -1297,7 +1380,9 @@ cudaError_t launch_cfg(const Params &P, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_after(prefill_kernel<T, C>, dim3((unsigned)(P.plan.cap_entries * P.g.groups)), C::THREADS, C::SMEM, st, P);
     if (e != cudaSuccess || !P.may_split) return e;
-    return launch_after(join_kernel<T, C::D>, dim3((unsigned)(P.plan.cap_items * P.g.groups), C::ROWS / 8), 256, 0, st, P);
+    const int64_t units = P.plan.cap_slots * P.g.groups * (C::ROWS / 8);
+    return launch_after(join_kernel<T, C::D>, dim3((unsigned)std::min<int64_t>(units, P.a.num_sms * kJoinPerSm)), 256, 0,
+                        st, P);
 }
 
 template <typename T>
