@@ -146,6 +146,19 @@ def test_few_rows_over_long_contexts(rows, dtype):
 
 @gpu
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("H,Hk,rows", [(64, 64, [3, 2]), (64, 32, [200, 150])])
+def test_unequal_contexts_of_many_heads(H, Hk, rows, dtype):
+    """As many items as SMs, of two lengths: cut finely, joined in an order of their own."""
+    import torch
+    from tests.gpu_helpers import device_status
+    c = Case(H, Hk, 64, 16, [8192, 4096], rows, dtype, seed=Hk)
+    c.checked(f"{H}/{Hk} heads")
+    assert torch.equal(c.run(), c.run())
+    assert device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
 def test_long_prompt(dtype):
     Case(4, 1, 128, 32, [2500, 1031], [2500, 900], dtype, seed=3).checked("long prompt")
 
