@@ -61,8 +61,10 @@ struct Cfg {
     static constexpr int KST = D == 64 ? 4 : 2;           // K tiles in shared memory
     static constexpr int VST = D == 256 ? 3 - NP : KST;
     static constexpr int DEPTH = 4;                       // scale tables
-    static constexpr int CONV = 4;                        // conversion warps
-    static constexpr int THREADS = 128 * (NS + 2);        // softmax, conversion, issue warpgroups
+    // Conversion warps.  Single: a job has twice the codes, and with 4 warps they were what it
+    // waited for (f16 552 -> 633 TFLOP/s, f32 468 -> 495 with 8).
+    static constexpr int CONV = NS == 1 ? 8 : 4;
+    static constexpr int THREADS = 128 * (NS + 1) + 32 * CONV;    // softmax, conversion, issue warpgroups
     static constexpr int ROWS = 128 * NT;
     static constexpr int FLUSH = NP == 2 ? kFlush : 1 << 29;   // 16-bit rows: never
     static constexpr uint32_t Q_PART = 128u * D * 2;      // bytes of one f16 part of one row tile
@@ -522,7 +524,8 @@ __device__ __forceinline__ uint4 chunk_of(const float *x) {
 // bounded and abortable):
 //  - softmax, one warpgroup per accumulator: a thread owns one row.  S row from
 //    TMEM -> z, mask, reference -> p -> p vs as f16 parts in TMEM.
-//  - conversion (4 warps): codes of the tile's tokens from global memory (a
+//  - conversion (4 warps; Single, whose jobs have twice the codes: 8): codes
+//    of the tile's tokens from global memory (a
 //    token's vector is one coalesced read; the next tile's words are in flight
 //    in registers) -> f16 tiles of 128-byte rows, K's for QK's B operand
 //    (K-major), V's for PV's (MN-major).
@@ -532,7 +535,7 @@ __device__ __forceinline__ uint4 chunk_of(const float *x) {
 //    by one thread as soon as S[n & 1] was read, and O += P V, by the other.
 //    S and P are apart, so a row's next logits are there when its weights are
 //    written, and the tensor core works on one job while two softmaxes run.
-// Barriers: k_full / v_full (4 conversion warps), t_full (the table
+// Barriers: k_full / v_full (the conversion warps), t_full (the table
 // warp), k_free / v_free (commit of the last MMA on a tile whose place is
 // needed again), t_free (the softmax warps that read the table), s_full[2]
 // (commit of QK), s_free[2] and p_full[2] (4 softmax warps), pv_done[2]
@@ -576,10 +579,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     if (warp == 0) tmem_alloc(s0 + C::BAR_OFF + C::BARS * 8, 512);
     if (tid == 32) {
         for (int i = 0; i < C::BARS; ++i) {
-            const bool by_warps = i < C::KST || (i >= 2 * C::KST && i < 2 * C::KST + C::VST) ||
-                                  (i >= B2 + 2 && i < B2 + 6);
+            const bool by_conv = i < C::KST || (i >= 2 * C::KST && i < 2 * C::KST + C::VST);
+            const bool by_softmax = i >= B2 + 2 && i < B2 + 6;
             const bool table = i >= BT + C::DEPTH && i < B2;
-            mbar_init(bars + 8 * i, table ? 4 * NS : by_warps ? 4 : 1);
+            mbar_init(bars + 8 * i, table ? 4 * NS : by_conv ? C::CONV : by_softmax ? 4 : 1);
         }
         *abort = 0u;
         fence_mbar_init();
@@ -716,12 +719,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     }
     bool issued = false;
 
-    if (warp >= 4 * NS + 4) {
+    constexpr int ISSUE = 4 * NS + C::CONV;                  // first warp of the issue warpgroup
+    if (warp >= ISSUE) {
         // -------------------------------------------------- issue and tables
         set_regs_down<NS == 2 ? 80 : 96>();
         // descriptors of the first tiles; offsets within and between tiles add to them in 16-byte units
         auto step_of = [](int job) { return C::MODE == kPair ? job >> 1 : job; };
-        if (warp == 4 * NS + 4 && elect_one()) {
+        if (warp == ISSUE && elect_one()) {
             constexpr uint32_t ID_QK = umma_idesc_f16(128, TN);
             const uint64_t dQ = swizzled_desc(s0 + C::Q_OFF, 16), dK = swizzled_desc(s0 + C::K_OFF, 16);
             for (int job = 0; job < jobs; ++job) {
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 if (last && j + C::KST < tiles) umma_commit(k_free(st));
                 issued = true;
             }
-        } else if (warp == 4 * NS + 5 && elect_one()) {
+        } else if (warp == ISSUE + 1 && elect_one()) {
             constexpr uint32_t ID_PV = umma_idesc_f16(128, D) | 1u << 16;       // B is MN-major
             const uint64_t dV = swizzled_desc(s0 + C::V_OFF, CT * 128);
             for (int job = 0; job < jobs; ++job) {
@@ -778,7 +782,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             }
         }
         __syncwarp();
-        if (warp == 4 * NS + 7) {
+        if (warp == ISSUE + 3) {
             // the rows of the CTA that comes to this place about next, on their way to L2 (bf16
             // pairs of tiles 797 -> 815 TFLOP/s, f32 rows 502 -> 522)
             const uint32_t next = (blockIdx.x + (uint32_t)a.num_sms) / P.g.groups;
@@ -797,7 +801,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                                  : "memory");
             }
         }
-        if (warp == 4 * NS + 6) {
+        if (warp == ISSUE + 2) {
             // tokens lane + 32 u of a tile; the next tile's scales and the pages of
             // the one after it are in flight
             constexpr int PER = CT / 32;
@@ -853,7 +857,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         }
     } else if (warp >= 4 * NS) {
         // ------------------------------------------------------- conversion
-        if (NS == 2) set_regs_down<112>();
+        set_regs_down<NS == 2 ? 112 : 104>();
         const int cw = warp - 4 * NS;
         constexpr int TPW = CT / C::CONV;                    // tokens of a tile per warp
         constexpr int NW = TPW * (W - 1) / 32;               // words of a tile per lane
@@ -933,7 +937,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         }
     } else {
         // ---------------------------------------------------------- softmax
-        // 2 x 160 + 112 + 80 = 4 x 128 registers a thread at launch; Single: 208 + 168 + 96 <= 3 x 168
+        // 2 x 160 + 112 + 80 = 208 + 2 x 104 + 96 = 4 x 128 registers a thread at launch
         set_regs_up<NS == 2 ? 160 : 208>();
         const int wg = warp >> 2;                            // accumulator
         const int rt = tid & 127;                            // row of the tile
