@@ -103,7 +103,7 @@ struct Plan {                          // in the workspace
     uint4 *items;                      // [cap_items]: seq, tile, K/V tiles, first slot
     uint4 *splits;                     // [cap_slots]: of the items in pieces: seq, tile, first slot, pieces
     float *part;                       // [slots][groups][ROWS][D + 4]
-    float *sums;                       // [SMs][accumulators][128][D], or none
+    float *sums;                       // [SMs][accumulators][D / 4][128][4], or none
     uint32_t *places;                  // a bit per place in sums: taken
     int64_t cap_items, cap_entries, cap_slots;
 };
@@ -609,7 +609,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     // whether accumulator x is flushed before the end
     auto flushes = [&](int x) { return NP == 2 && (C::MODE == kSingle ? jobs : (jobs - x + 1) / 2) > C::FLUSH; };
     if (flushes(0) && tid == 0) {
-        uint32_t p = 0;
+        // the SM's own place is free, unless its number is not below the count of SMs (CTAs that
+        // all looked from place 0 on queued for it: a kernel that flushes took half again as long)
+        uint32_t p;
+        asm("mov.u32 %0, %%smid;" : "=r"(p));
+        p %= (uint32_t)a.num_sms;
         for (int tries = 0;; p = (p + 1) % (uint32_t)a.num_sms) {
             if (!(atomicOr(P.plan.places + p / 32, 1u << (p & 31)) >> (p & 31) & 1u)) break;
             if (++tries > 1 << 20) {                         // never with one CTA per SM
@@ -954,11 +958,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         float R = -INFINITY, Rs = -INFINITY;                 // references of the accumulator and of the sums
         float2 l2 = make_float2(0.0f, 0.0f);
         bool ok = true, flushed = false;
-        // the row's sums of accumulator x
+        // the row's sums of accumulator x: four columns of the 128 rows together, so that a warp's
+        // accesses are whole lines
         auto sums_of = [&](int x) {
-            return P.plan.sums + (((int64_t)*place * NS + x) * 128 + rt) * D;
+            return reinterpret_cast<float4 *>(P.plan.sums + ((int64_t)*place * NS + x) * 128 * D) + rt;
         };
-        float *sums = flushes(0) ? sums_of(C::MODE == kSingle ? 0 : wg) : nullptr;
+        float4 *sums = flushes(0) ? sums_of(C::MODE == kSingle ? 0 : wg) : nullptr;
         auto tile_job = [&](auto mask_c, int job, int step, int b) {
             constexpr bool MASK = decltype(mask_c)::value;
             const int tab = step / SUB % C::DEPTH, sub = step % SUB;
@@ -1091,18 +1096,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 ok = wait_for(pv_done(before & 1), (before >> 1) & 1, abort);
                 if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
                 tc_fence_after();
+                // without waiting for the sums where no row of the warp has a new reference: this
+                // thread alone adds to its places, so in a fixed order
                 const float f = Rs == R ? 1.0f : fast_exp2(Rs - R);
+                const bool same = __all_sync(0xFFFFFFFFu, f == 1.0f);
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     float o[32];
-                    float4 *at = reinterpret_cast<float4 *>(sums + k), s4[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) s4[x] = flushed ? at[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    float4 *at = sums + k / 4 * 128;
                     tmem_ld32(tOw + k, o);
+                    if (flushed && same) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        at[x] = make_float4(fmaf(s4[x].x, f, o[4 * x]), fmaf(s4[x].y, f, o[4 * x + 1]),
-                                            fmaf(s4[x].z, f, o[4 * x + 2]), fmaf(s4[x].w, f, o[4 * x + 3]));
+                        for (int x = 0; x < 8; ++x)
+                            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at + x * 128), "f"(o[4 * x]),
+                                         "f"(o[4 * x + 1]), "f"(o[4 * x + 2]), "f"(o[4 * x + 3])
+                                         : "memory");
+                        continue;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        float4 v = flushed ? __ldcg(at + x * 128) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        v = make_float4(fmaf(v.x, f, o[4 * x]), fmaf(v.y, f, o[4 * x + 1]), fmaf(v.z, f, o[4 * x + 2]),
+                                        fmaf(v.w, f, o[4 * x + 3]));
+                        __stcg(at + x * 128, v);
+                    }
                 }
                 Rs = R;
                 flushed = true;
@@ -1162,10 +1179,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 tmem_ld32((C::MODE == kSplit ? tO + x * D + lanes : tOw) + k, o);
                 if constexpr (NP == 2) {
                     if (!flushes(x)) return;
-                    const float4 *at = reinterpret_cast<const float4 *>(sums_of(x) + k);
+                    const float4 *at = sums_of(x) + k / 4 * 128;
 #pragma unroll
                     for (int y = 0; y < 8; ++y) {
-                        const float4 v = at[y];
+                        const float4 v = __ldcg(at + y * 128);
                         o[4 * y] = fmaf(v.x, g, o[4 * y]);
                         o[4 * y + 1] = fmaf(v.y, g, o[4 * y + 1]);
                         o[4 * y + 2] = fmaf(v.z, g, o[4 * y + 2]);
