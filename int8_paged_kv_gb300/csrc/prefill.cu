@@ -78,6 +78,14 @@ struct Cfg {
     static constexpr int CONV = NS == 1 ? 8 : 4;
     static constexpr int THREADS = 128 * (NS + 1) + 32 * CONV;    // softmax, conversion, issue warpgroups
     static constexpr int ROWS = 128 * NT;
+    // Registers a thread by role, 4 x 128 in all, the threads' share at launch.  Each kernel has the
+    // split in which the compiler spills none (the other one: head size 64, f32 461 us for 423,
+    // bf16 579 for 562; head size 128, Pair 1% more, f32 13%).
+    static constexpr bool WIDE = D == 128 && (MODE == kPair || NP == 2);
+    static constexpr int REGS_SOFTMAX = MODE == kSingle ? 208 : 160;
+    static constexpr int REGS_CONV = WIDE ? 112 : 104;
+    static constexpr int REGS_ISSUE = MODE == kSingle ? 96 : WIDE ? 80 : 88;
+    static_assert(NS * REGS_SOFTMAX + CONV / 4 * REGS_CONV + REGS_ISSUE <= 512, "registers at launch");
     static constexpr int FLUSH = NP == 2 ? kFlush : 1 << 29;   // 16-bit rows: never
     static constexpr uint32_t Q_PART = 128u * D * 2;      // bytes of one f16 part of one row tile
     static constexpr uint32_t KV_TILE = (uint32_t)CT * D * 2;
@@ -742,7 +750,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     constexpr int ISSUE = 4 * NS + C::CONV;                  // first warp of the issue warpgroup
     if (warp >= ISSUE) {
         // -------------------------------------------------- issue and tables
-        set_regs_down<NS == 2 ? 80 : 96>();
+        set_regs_down<C::REGS_ISSUE>();
         // descriptors of the first tiles; offsets within and between tiles add to them in 16-byte units
         auto step_of = [](int job) { return C::MODE == kPair ? job >> 1 : job; };
         if (warp == ISSUE && elect_one()) {
@@ -877,7 +885,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         }
     } else if (warp >= 4 * NS) {
         // ------------------------------------------------------- conversion
-        set_regs_down<NS == 2 ? 112 : 104>();
+        set_regs_down<C::REGS_CONV>();
         const int cw = warp - 4 * NS;
         constexpr int TPW = CT / C::CONV;                    // tokens of a tile per warp
         constexpr int NW = TPW * (W - 1) / 32;               // words of a tile per lane
@@ -957,8 +965,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
         }
     } else {
         // ---------------------------------------------------------- softmax
-        // 2 x 160 + 112 + 80 = 208 + 2 x 104 + 96 = 4 x 128 registers a thread at launch
-        set_regs_up<NS == 2 ? 160 : 208>();
+        set_regs_up<C::REGS_SOFTMAX>();
         const int wg = warp >> 2;                            // accumulator
         const int rt = tid & 127;                            // row of the tile
         const int nt = C::MODE == kPair ? wg : 0;
