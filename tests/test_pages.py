@@ -288,6 +288,52 @@ def test_copies(cache, Hk, B, D):
 
 
 @gpu
+def test_long_lists_of_copies():
+    """More pairs than one round of lookups takes, two thirds of them padding; some ids that do not exist."""
+    import torch
+    import int8_paged_kv_gb300 as pk
+    nb, n = 70001, 69000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache = [torch.randint(-2 ** 31, 2 ** 31 - 1, (nb, 1, 4, 17), dtype=torch.int32, device="cuda", generator=g)
+             for _ in range(2)]
+    perm = torch.randperm(nb, device="cuda", generator=g).to(torch.int32)
+    src, dst = perm[:23000], perm[23000:46000]
+    at = torch.randperm(n, device="cuda", generator=g)[:23000]
+    lists = [torch.full((n,), -1, dtype=torch.int32, device="cuda") for _ in range(2)]
+    lists[0][at], lists[1][at] = src, dst
+    want = [c.clone() for c in cache]
+    for c in want:
+        c[dst.long()] = c[src.long()]
+    pk.pa_q8_copy_blocks(*cache, *lists)
+    assert all(torch.equal(x, y) for x, y in zip(cache, want)) and pk.pa_q8_device_status() == 0
+    lists[0][at[7]] = nb
+    pk.pa_q8_copy_blocks(*cache, *lists)
+    assert all(torch.equal(x, y) for x, y in zip(cache, want))
+    assert pk.pa_q8_device_status() == pk.PA_Q8_DEV_BAD_BLOCK
+
+
+@gpu
+@pytest.mark.parametrize("rows", [3, 700])
+def test_rows_freed_many_times_in_one_call(rows):
+    """Each row is freed once, wherever the call names it; rows out of range between them are flagged."""
+    import torch
+    import int8_paged_kv_gb300 as pk
+    pool = Pool(rows, 9, rows * 8, 16)
+    everyone = torch.arange(rows, dtype=torch.int32, device="cuda")
+    pk.pa_q8_extend_seqs(*pool.all, everyone, torch.full_like(everyone, 128), block_size=16)
+    assert int(pool.count) == 0
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    seqs = torch.cat([everyone[: rows - 1].repeat(40), u32([rows, 0xFFFFFFFF])])
+    pk.pa_q8_free_seqs(*pool.all, seqs[torch.randperm(len(seqs), device="cuda", generator=g)].contiguous(), block_size=16)
+    held = pool.table[rows - 1, :8]
+    assert int(pool.count) == (rows - 1) * 8 and pool.lens.tolist() == [0] * (rows - 1) + [128]
+    stack = pool.stack[: (rows - 1) * 8]
+    assert torch.equal(stack, torch.sort(stack)[0]) and not torch.isin(stack, held).any()
+    assert int(pool.refs.sum()) == 8 and bool((pool.refs[held.long()] == 1).all())
+    assert pk.pa_q8_device_status() == pk.PA_Q8_DEV_BAD_SEQ
+
+
+@gpu
 def test_copies_past_32bit_offsets():
     """Pages whose words lie past 2^32 (18.6 GB per cache), and a list much longer than the grid."""
     import torch
