@@ -111,15 +111,11 @@ struct Cfg {
     static_assert(TM_Q + NT * NP * QT * 32 <= 512, "TMEM");
 };
 
-// One CTA's work: rows of a tile of a sequence against K/V tiles [j0, j1).
-struct Item {
-    uint32_t seq, tile, j0, slot;     // slot: its partial record, when the item is split
-};
-
 struct Plan {                          // in the workspace
-    uint32_t *head;                    // entries, items, K/V tiles that pay for a piece, split items
+    uint32_t *head;                    // entries, K/V tiles that pay for a piece, split items
     uint32_t *first;                   // [num_seqs + 1] items before a sequence's first
-    uint4 *entries;                    // [cap_entries], most K/V tiles first
+    uint4 *entries;                    // [cap_entries], most K/V tiles first: a CTA's work per kv head slice: seq,
+                                       // row tile, first K/V tile, slot of its record (none: the whole item)
     uint4 *items;                      // [cap_items]: seq, tile, K/V tiles, first slot
     uint4 *splits;                     // [cap_slots]: of the items in pieces: seq, tile, first slot, pieces
     float *part;                       // [slots][groups][ROWS][D + 4]
@@ -357,9 +353,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
     }
     if (tid == 0) {
         P.plan.head[0] = (uint32_t)min((int64_t)entries, P.plan.cap_entries);
-        P.plan.head[1] = items;
-        P.plan.head[2] = piece;
-        P.plan.head[3] = splits;
+        P.plan.head[1] = piece;
+        P.plan.head[2] = splits;
     }
 }
 
@@ -626,7 +621,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     const int seen_all = most_seen(c, n, e.y * P.g.span, P.g.span);
     const int j0 = (int)e.z;
     uint32_t piece_len;
-    pieces_of((uint32_t)(seen_all + CT - 1) / CT, P.plan.head[2], piece_len);
+    pieces_of((uint32_t)(seen_all + CT - 1) / CT, P.plan.head[1], piece_len);
     const int tiles = min((seen_all + CT - 1) / CT - j0, (int)piece_len);
     const int steps = min(tiles * SUB, (seen_all + TN - 1) / TN - j0 * SUB);     // of TN tokens
     const int jobs = C::MODE == kPair ? 2 * steps : steps;
@@ -1312,7 +1307,7 @@ __global__ void __launch_bounds__(256) join_kernel(Params P) {
     const PrefillArgs &a = P.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t per = P.rows / 8;                         // CTAs of one piece's rows
-    const uint64_t units = (uint64_t)P.plan.head[3] * P.g.groups * per;
+    const uint64_t units = (uint64_t)P.plan.head[2] * P.g.groups * per;
     for (uint64_t u = blockIdx.x; u < units; u += gridDim.x) {
         const int r = (int)(u % per) * 8 + warp;
         const uint32_t cta = (uint32_t)(u / per) % P.g.groups;
