@@ -478,20 +478,32 @@ def _queue(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _allocate(need, like, stream):
+    """`need` bytes on the device of the tensor `like`, from the pool of the
+    stream that will use them: torch gives a stream's memory away again behind
+    the work queued there, so what is freed once a call has queued its work
+    needs no event, and no other stream's work is pending on it."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1: the legacy default stream (an ExternalStream(0) is a new stream)
+        stream = (torch.cuda.default_stream(like.device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=like.device))
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
 def _scratch(need, workspace, like, stream):
-    """(address, bytes) of the caller's workspace, or of one allocated here and
-    kept from reuse until the work queued on `stream` is done with it; `like`:
-    a tensor on the call's device."""
+    """(tensor, address, bytes) of the caller's workspace, or of one allocated
+    here; `like`: a tensor on the call's device.  The caller holds the tensor
+    until the library has queued its work: its memory is given away when it goes."""
     if workspace is None:
-        import torch
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            workspace.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int)
-                                    else stream)
-        return workspace.data_ptr(), max(need, 16)
-    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        workspace = _allocate(max(need, 16), like, stream)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _row_type(dtype):
@@ -537,7 +549,7 @@ def pa_q8_prefill(out, q, key_cache, value_cache, block_tables, context_lens, qu
     u32 = _U32
     L = lib()
     need = L.pa_q8_prefill_workspace_size(T, S, H, num_kv_heads, D, block_size, Nb, dt)
-    ws, ws_bytes = _scratch(need, workspace, q, stream)
+    scratch, ws, ws_bytes = _scratch(need, workspace, q, stream)
     _check("pa_q8_prefill", L.pa_q8_prefill(
         out.data_ptr(), q.data_ptr(), dt, os_, qs, _address(key_cache, u32, "key_cache", dev),
         _address(value_cache, u32, "value_cache", dev, words), _address(block_tables, u32, "block_tables", dev),
@@ -611,7 +623,7 @@ def pa_q8_extend_seqs(block_tables, context_lens, ref_counts, free_blocks, num_f
     n = seqs.numel()
     L = lib()
     u32 = _U32
-    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
+    scratch, ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
     _check("pa_q8_extend_seqs", L.pa_q8_extend_seqs(
         *pool, _address(seqs, u32, "seqs", dev), _address(new_lens, u32, "new_lens", dev, n), n, S, Nb,
         block_size, nb, ws, ws_bytes, _queue(stream, dev)))
@@ -625,7 +637,7 @@ def pa_q8_fork_seqs(block_tables, context_lens, ref_counts, free_blocks, num_fre
     n = parents.numel()
     L = lib()
     u32 = _U32
-    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
+    scratch, ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, n), workspace, block_tables, stream)
     _check("pa_q8_fork_seqs", L.pa_q8_fork_seqs(
         *pool, _address(parents, u32, "parents", dev), _address(children, u32, "children", dev, n),
         _address(copy_src, u32, "copy_src", dev, n), _address(copy_dst, u32, "copy_dst", dev, n), n, S, Nb,
@@ -648,7 +660,7 @@ def pa_q8_compact_blocks(block_tables, context_lens, ref_counts, free_blocks, nu
     n = move_src.numel()
     L = lib()
     u32 = _U32
-    ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, 0), workspace, block_tables, stream)
+    scratch, ws, ws_bytes = _scratch(L.pa_q8_pool_workspace_size(S, nb, 0), workspace, block_tables, stream)
     _check("pa_q8_compact_blocks", L.pa_q8_compact_blocks(
         *pool, _address(move_src, u32, "move_src", dev), _address(move_dst, u32, "move_dst", dev, n), n, S, Nb,
         block_size, nb, ws, ws_bytes, _queue(stream, dev)))
