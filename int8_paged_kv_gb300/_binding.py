@@ -163,6 +163,23 @@ def _opts(kernel: int, partition_tokens: int):
     return ctypes.byref(DecodeOptions(int(kernel), int(partition_tokens)))
 
 
+def _allocate(need, like, stream):
+    """`need` bytes on the device of the tensor `like`, from the pool of the
+    stream that will use them: torch gives a stream's memory away again behind
+    the work queued there, so what is freed once a call has queued its work
+    needs no event, and no other stream's work is pending on it."""
+    import torch
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        # 0 and 1: the legacy default stream (an ExternalStream(0) is a new stream)
+        stream = (torch.cuda.default_stream(like.device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=like.device))
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
+
+
 def pa_q8_reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, *, num_kv_heads: int,
                             head_size: int, block_size: int, num_blocks: int | None = None,
                             stream=None) -> None:
@@ -233,7 +250,7 @@ def pa_q8_decode(out, q, key_cache, value_cache, block_tables, context_lens, *, 
     need = pa_q8_decode_workspace_size(S, H, num_kv_heads, D, block_size, Nb, kernel=kernel,
                                        partition_tokens=partition_tokens)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(need, q, stream)
     ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace is not None else ctypes.c_void_p(0)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = lib().pa_q8_decode_ex(
@@ -273,7 +290,7 @@ def pa_q8_decode_rows(out, q, key_cache, value_cache, block_tables, context_lens
     need = pa_q8_decode_rows_workspace_size(S, R, H, num_kv_heads, D, block_size, Nb, kernel=kernel,
                                             partition_tokens=partition_tokens)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(need, q, stream)
     ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace is not None else ctypes.c_void_p(0)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = lib().pa_q8_decode_rows(
@@ -319,7 +336,7 @@ def pa_q8_decode_append(out, q, key, value, key_cache, value_cache, block_tables
     need = pa_q8_decode_rows_workspace_size(S, R, H, num_kv_heads, D, block_size, Nb, kernel=kernel,
                                             partition_tokens=partition_tokens)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(need, q, stream)
     ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace is not None else ctypes.c_void_p(0)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = lib().pa_q8_decode_append(
@@ -373,7 +390,7 @@ def pa_f32_decode(out, q, key_cache, value_cache, block_tables, context_lens, *,
     need = pa_f32_decode_workspace_size(S, H, num_kv_heads, D, block_size, Nb,
                                         partition_tokens=partition_tokens)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(need, q, stream)
     ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace is not None else ctypes.c_void_p(0)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = lib().pa_f32_decode(
@@ -424,7 +441,7 @@ def pa_q8c_decode(out, q, key_cache, value_cache, context_lens, *, num_kv_heads:
         raise ValueError("context_lens does not match num_seqs")
     need = pa_q8c_decode_workspace_size(S, H, num_kv_heads, D, max_t, partition_tokens=partition_tokens)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _allocate(need, q, stream)
     ws_ptr = ctypes.c_void_p(workspace.data_ptr()) if workspace is not None else ctypes.c_void_p(0)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     rc = lib().pa_q8c_decode(
@@ -476,23 +493,6 @@ def _queue(stream, device):
     if stream is None:
         return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _allocate(need, like, stream):
-    """`need` bytes on the device of the tensor `like`, from the pool of the
-    stream that will use them: torch gives a stream's memory away again behind
-    the work queued there, so what is freed once a call has queued its work
-    needs no event, and no other stream's work is pending on it."""
-    import torch
-    if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-        # 0 and 1: the legacy default stream (an ExternalStream(0) is a new stream)
-        stream = (torch.cuda.default_stream(like.device) if handle in (0, 1)
-                  else torch.cuda.ExternalStream(handle, device=like.device))
-    with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 
 def _scratch(need, workspace, like, stream):

@@ -82,26 +82,34 @@ def pool_and_caches():
 def calls(names, b, **kw):
     i32, pool, cache, q = pool_and_caches()
     one, sizes = i32(1), dict(num_kv_heads=2, block_size=16, scale=0.1)
-    rows = q[:, None]
+    rows = q[:, None].contiguous()
     every = {
         "prefill": lambda: b.pa_q8_prefill(q.clone(), q, cache, cache, pool[0], pool[1], i32(5), **sizes, **kw),
         "extend": lambda: b.pa_q8_extend_seqs(*pool, one, one, block_size=16, **kw),
         "fork": lambda: b.pa_q8_fork_seqs(*pool, one, one, one, one, block_size=16, **kw),
         "compact": lambda: b.pa_q8_compact_blocks(*pool, i32(8), i32(8), block_size=16, **kw),
+        "decode": lambda: b.pa_q8_decode(q.clone(), q, cache, cache, pool[0], pool[1], **sizes, **kw),
+        "decode_rows": lambda: b.pa_q8_decode_rows(rows.clone(), rows, cache, cache, pool[0], pool[1], **sizes, **kw),
+        "decode_append": lambda: b.pa_q8_decode_append(rows.clone(), rows, q[:, None, :2].contiguous(),
+                                                       q[:, None, :2].contiguous(), cache, cache, pool[0], pool[1],
+                                                       **sizes, **kw),
+        "f32_decode": lambda: b.pa_f32_decode(q.clone(), q, cache, cache, pool[0], pool[1], **sizes, **kw),
+        "q8c_decode": lambda: b.pa_q8c_decode(q.clone(), q, cache, cache, pool[1], num_kv_heads=2, max_t=64, scale=0.1,
+                                              **kw),
     }
     return every[names]
 
 
-NEW = ["prefill", "extend", "fork", "compact"]
+EVERY = ["prefill", "extend", "fork", "compact", "decode", "decode_rows", "decode_append", "f32_decode", "q8c_decode"]
 
 
-@pytest.mark.parametrize("name", NEW)
+@pytest.mark.parametrize("name", EVERY)
 def test_the_workspace_lives_until_the_call_is_queued(stand_in, name):
     calls(name, stand_in.binding)()
     assert stand_in.library.alive == [[None]]
 
 
-@pytest.mark.parametrize("name", NEW)
+@pytest.mark.parametrize("name", EVERY)
 def test_the_workspace_comes_from_the_streams_own_pool(stand_in, monkeypatch, name):
     import torch
     side = types.SimpleNamespace(cuda_stream=64)
