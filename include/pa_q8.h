@@ -308,8 +308,10 @@ size_t pa_q8_decode_rows_workspace_size(int num_seqs, int num_rows, int num_head
  *                   PA_Q8_DEV_BAD_ROWS; one with no rows does nothing
  *   num_rows        rows of q and out; 0 is a no-op
  *   workspace       >= pa_q8_prefill_workspace_size() bytes, 16-byte aligned
- * Every other argument is that of pa_q8_decode; block ids >= num_blocks are
- * skipped and flagged.  The softmax runs in f32.  f32 rows keep 22 bits of q
+ * Every other argument is that of pa_q8_decode.  A token in a block whose id is
+ * >= num_blocks counts as one whose K and V are zeros (a logit of 0, which takes
+ * weight from the others), and is flagged PA_Q8_DEV_BAD_BLOCK: rows that see such
+ * a token are of no use.  The softmax runs in f32.  f32 rows keep 22 bits of q
  * and of the weights through the tensor cores (two f16 parts each), f16 and
  * bf16 rows 11 (one part); with those the tensor cores' accumulators, which
  * cut their last bit, add about 1.2e-9 of the result per context token (1.5e-4

@@ -21,7 +21,10 @@
 // Sums of p and all accumulators are f32.
 //
 // Masks.  A token that a row does not see has p = 0 by selection, whatever its
-// words hold, and does not enter the row's reference.
+// words hold, and does not enter the row's reference.  A token on a page that does
+// not exist gets zero scales, so it counts as zero vectors.  (Masked out by a bit
+// per token, every call would take longer: bf16 pairs of tiles 0.3%, f32 rows and
+// head size 256 1.3 to 1.6%.)
 //
 // Rates, causal operations (4 per row, head, dimension and token seen) over the
 // call's time, whole prompts of up to 4096 tokens, 32 heads on 8, head size 128:
