@@ -356,8 +356,9 @@ int pa_q8_pool_init(uint32_t *ref_counts, uint32_t *free_blocks, uint32_t *num_f
  * order and appended to its row, context_lens becomes new_lens[i].  A length
  * not above the present one changes nothing.  Flagged and skipped: seqs[i] >=
  * num_seqs, a row named by an earlier request, a length beyond the row
- * (BAD_SEQ); a request that together with those before it needs more pages
- * than are free (NO_BLOCK). */
+ * (BAD_SEQ); a request for pages that together with those before it, refused
+ * ones among them, needs more than are free (NO_BLOCK).  Growth within a row's
+ * last page needs none and is never refused for want of one. */
 int pa_q8_extend_seqs(uint32_t *block_tables, uint32_t *context_lens, uint32_t *ref_counts,
                       uint32_t *free_blocks, uint32_t *num_free, const uint32_t *seqs,
                       const uint32_t *new_lens, int num_requests, int num_seqs,

@@ -269,7 +269,8 @@ fork_rows_kernel(PoolArgs a, const uint32_t *parents, const uint32_t *children, 
 }
 
 // ---- extend: pages for a sequence's tokens up to a new length, popped in
-// request order.  info[i]: pages held, pages added, the stack's top for it.
+// request order; growth within the last page needs none, whatever was refused
+// before.  info[i]: pages held, pages added, the stack's top for it.
 __global__ void __launch_bounds__(kPlanThreads)
 extend_plan_kernel(PoolArgs a, const uint32_t *seqs, const uint32_t *new_lens, int n, uint32_t *claim, uint4 *info) {
     claim_rows(a, seqs, n, claim);
@@ -295,7 +296,7 @@ extend_plan_kernel(PoolArgs a, const uint32_t *seqs, const uint32_t *new_lens, i
         unsigned long long total;
         const unsigned long long start = base + scan_cta(need, total);
         base += total;
-        const bool fits = start + need <= top;
+        const bool fits = need == 0 || start + need <= top;
         if (grows && !fits) {
             flag_error(a.status, kDevNoBlock);
             need = 0;
