@@ -307,7 +307,12 @@ size_t pa_q8_decode_rows_workspace_size(int num_seqs, int num_rows, int num_head
  *                   its own or ends behind num_rows is skipped and flagged
  *                   PA_Q8_DEV_BAD_ROWS; one with no rows does nothing
  *   num_rows        rows of q and out; 0 is a no-op
- *   workspace       >= pa_q8_prefill_workspace_size() bytes, 16-byte aligned
+ *   workspace       >= pa_q8_prefill_workspace_size() bytes, 16-byte aligned.  What the
+ *                   tables could hold (max_blocks_per_seq * block_size) counts, not the
+ *                   lengths: lists of about 16 bytes per 128 (row, head) pairs of a kv
+ *                   head; for f32 rows 10 to 20 MB of sums when a row can hold more than
+ *                   1024 tokens; and, when few rows can meet contexts long enough to be
+ *                   cut into pieces, the pieces' records: 4 to 170 MB
  * Every other argument is that of pa_q8_decode.  A token in a block whose id is
  * >= num_blocks counts as one whose K and V are zeros (a logit of 0, which takes
  * weight from the others), and is flagged PA_Q8_DEV_BAD_BLOCK: rows that see such

@@ -1413,8 +1413,8 @@ size_t layout(const PrefillArgs &a, Params &P) {
     p.splits = reinterpret_cast<uint4 *>(take((size_t)p.cap_slots * 16));
     p.part = reinterpret_cast<float *>(take((size_t)p.cap_slots * g.groups * P.rows * (a.head_size + 4) * 4));
     p.places = reinterpret_cast<uint32_t *>(take((size_t)(a.num_sms + 31) / 32 * 4));
-    // (a context short of the shortest flush needs no sums)
-    const bool sums = (int64_t)a.max_blocks_per_seq * a.block_size > kFlush * kTN;
+    // (16-bit rows never flush, nor does a context short of the shortest flush)
+    const bool sums = a.dtype == PA_Q8_F32 && room > kFlush * kTN;
     p.sums = reinterpret_cast<float *>(
         take(sums ? (size_t)a.num_sms * (a.head_size == 256 ? 1 : 2) * 128 * a.head_size * 4 : 0));
     return at;
