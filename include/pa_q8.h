@@ -316,11 +316,20 @@ size_t pa_q8_decode_rows_workspace_size(int num_seqs, int num_rows, int num_head
  * Every other argument is that of pa_q8_decode.  A token in a block whose id is
  * >= num_blocks counts as one whose K and V are zeros (a logit of 0, which takes
  * weight from the others), and is flagged PA_Q8_DEV_BAD_BLOCK: rows that see such
- * a token are of no use.  The softmax runs in f32.  f32 rows keep 22 bits of q
- * and of the weights through the tensor cores (two f16 parts each), f16 and
- * bf16 rows 11 (one part); with those the tensor cores' accumulators, which
- * cut their last bit, add about 1.2e-9 of the result per context token (1.5e-4
- * at 131072 tokens).  num_heads / num_kv_heads up to 4096.
+ * a token are of no use.  num_heads / num_kv_heads up to 4096.
+ *
+ * Precision.  The softmax and all sums are f32.  Through the tensor cores an
+ * element of q goes as two f16 parts (f32 rows: 22 bits) or one (f16 and bf16
+ * rows: all of its 11 or 8), no finer than 2^-25 of its row's largest.  A
+ * token's weight times its V scale goes the same way, 2^-22 or 2^-11 of itself
+ * off, but no finer than 2^-32 of the largest weight times the largest V scale
+ * among any 64 tokens that the row has met: a token whose V is many powers of
+ * two larger hides the others near it, even when its own weight is small.  The
+ * accumulators lose, toward zero, about 1e-7 of what they hold per 16 tokens.
+ * f32 rows, whose accumulators are emptied into f32 sums after every 1024
+ * tokens, are off by that up to 1.2e-5 of the result at any length (2e-6 with V
+ * around zero); 16-bit rows by up to 6e-9 per context token (8e-4 at 131072
+ * tokens when the first ones have nearly all weight; 7e-5 with V around zero).
  */
 int pa_q8_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64_t q_stride,
                   const uint32_t *key_cache, const uint32_t *value_cache,

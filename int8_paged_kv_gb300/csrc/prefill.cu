@@ -16,9 +16,10 @@
 // 2^-25 of the row's largest value, and f32 rows keep 22 bits in two.  The
 // weight that meets the code of token t is p_t vs_t (vs: the token's V scale),
 // rounded to one f16 (16-bit rows: 2^-11 of itself, below their own rounding)
-// or two (f32 rows).  R moves with the scales too: the tile's largest p vs
-// stays below 2^15, and R is raised only when it must be, then to leave 2^7.
-// Sums of p and all accumulators are f32.
+// or two (f32 rows: 2^-22), neither finer than 2^-25.  R moves with the scales too:
+// a job's largest p times its largest vs stays below 2^15, and R is raised only when
+// it must be, then to leave 2^7; so 2^-25 is at most 2^-32 of the largest such
+// product, whatever the weight.  Sums of p and all accumulators are f32.
 //
 // Masks.  A token that a row does not see has p = 0 by selection, whatever its
 // words hold, and does not enter the row's reference.  A token on a page that does
@@ -55,8 +56,10 @@ namespace {
 // Single: one row tile and one accumulator (head size 256 fills TMEM).
 enum Mode { kPair, kSplit, kSingle };
 
-// Jobs after which an accumulator of f32 rows is added to sums of its own: at
-// most 5e-6 of what it holds was cut off by then, where all terms have one sign.
+// Jobs after which an accumulator of f32 rows is added to sums of its own.  A job is
+// 8 steps (MMAs of 16 tokens), and each cuts off about 1e-7 of what the accumulator
+// holds where all terms have one sign: 1.2e-5 at a flush when nearly all weight came
+// with the first job, a third of that when it came evenly.
 constexpr int kFlush = 16;
 
 // 64 tokens a job leave room in TMEM for the weights beside the logits.
@@ -561,12 +564,14 @@ __device__ __forceinline__ uint4 chunk_of(const float *x) {
 // (commit of QK), s_free[2] and p_full[2] (4 softmax warps), pv_done[2]
 // (commit of PV).
 //
-// The tensor cores cut an accumulator's last bit at every step, always toward
-// zero, which adds up over a long context (f32 rows, 130,000 tokens: 1.5e-4 of
-// the result, which 16-bit rows can bear).  So with f32 rows, every FLUSH jobs
-// the softmax warps add the accumulator to f32 sums in the workspace and PV starts
-// it anew: 2e-6, a third of a plain f32 evaluation's.  (Every 32 jobs: 4e-6, and
-// 7% faster; every 8: 1e-6, 13% slower.)  There are as many places for sums as
+// The tensor cores cut what they add at an accumulator's last bits, always toward
+// zero, about 1e-7 of it at every step, which adds up over a long context that one CTA
+// walks (131,072 tokens: 4e-4 to 7e-4 of the result for V with a mean, 8e-4 when the
+// first tokens have nearly all weight, 7e-5 for V around zero).  16-bit rows are left
+// with that.  With f32 rows, every FLUSH jobs the softmax warps add the accumulator to
+// f32 sums in the workspace and PV starts it anew: 3.6e-6, 1.2e-5 and 2.1e-6, at any
+// length.  (Every 32 jobs: twice that, and 7% faster; every 8: half, 13% slower.)
+// There are as many places for sums as
 // SMs, each of which has one CTA at a time; a CTA takes a free one and gives it
 // back.
 template <typename T, typename C>
