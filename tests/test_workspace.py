@@ -128,6 +128,19 @@ def test_streams_given_by_their_handle(stand_in, monkeypatch, handle, default):
     assert stand_in.library.alive == [["default" if default else handle]]
 
 
+def test_no_private_call_of_torch_is_needed(monkeypatch):
+    """Without torch's short way to a stream's handle its public functions give it."""
+    import torch
+    from int8_paged_kv_gb300 import _binding
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(_binding, "_current_device", None)
+    monkeypatch.setattr(_binding, "_raw_stream", None)
+    with pytest.raises(TypeError, match="CUDA tensors"):
+        _binding._current(torch.zeros(1))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=100 + device))
+    assert _binding._queue(None, 3) == 103 and _binding._queue(7, 3) == 7
+
+
 @gpu
 def test_two_streams_with_work_pending():
     """Calls that leave the workspace to the binding, on two streams at once and behind writes that are
