@@ -252,37 +252,28 @@ int copy_blocks_impl(uint32_t *key_cache, uint32_t *value_cache, const uint32_t 
 
 int dtype_bytes(int dtype) { return dtype == PA_Q8_F32 ? 4 : 2; }
 
-int check_prefill_shape(int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads, int head_size,
-                        int block_size, int max_blocks_per_seq, int dtype) {
+void prefill_fill(pa_q8::PrefillArgs &a, int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads,
+                  int head_size, int block_size, int max_blocks_per_seq, int dtype) {
+    std::memset(&a, 0, sizeof a);
+    a.dtype = dtype;
+    a.num_rows = num_rows;
+    a.num_seqs = num_seqs;
+    a.num_heads = num_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_size = head_size;
+    a.block_size = block_size;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    if (device_info(nullptr, &a.num_sms) != PA_Q8_OK) a.num_sms = 152;   // a size query or refusal without a device
+}
+
+int check_prefill_shape(pa_q8::PrefillArgs &a, int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads,
+                        int head_size, int block_size, int max_blocks_per_seq, int dtype) {
     if (num_rows < 0 || dtype < PA_Q8_F32 || dtype > PA_Q8_BF16) return PA_Q8_EINVAL;
     const int rc = check_decode_shape(num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq);
     if (rc != PA_Q8_OK) return rc;
     if (num_rows > (int64_t)1 << 30 || num_heads / num_kv_heads > 4096) return PA_Q8_EUNSUPPORTED;
-    pa_q8::PrefillArgs a;
-    std::memset(&a, 0, sizeof a);
-    a.dtype = dtype;
-    a.num_rows = num_rows;
-    a.num_seqs = num_seqs;
-    a.num_heads = num_heads;
-    a.num_kv_heads = num_kv_heads;
-    a.head_size = head_size;
-    a.block_size = block_size;
-    a.max_blocks_per_seq = max_blocks_per_seq;
+    prefill_fill(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, dtype);
     return pa_q8::prefill_ctas(a) > 0x7FFFFFFF ? PA_Q8_EUNSUPPORTED : PA_Q8_OK;   // grid x
-}
-
-void prefill_fill(pa_q8::PrefillArgs &a, int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads,
-                  int head_size, int block_size, int max_blocks_per_seq, int dtype, int sms) {
-    std::memset(&a, 0, sizeof a);
-    a.dtype = dtype;
-    a.num_rows = num_rows;
-    a.num_seqs = num_seqs;
-    a.num_heads = num_heads;
-    a.num_kv_heads = num_kv_heads;
-    a.head_size = head_size;
-    a.block_size = block_size;
-    a.max_blocks_per_seq = max_blocks_per_seq;
-    a.num_sms = sms;
 }
 
 }  // namespace
@@ -544,13 +535,10 @@ int pa_q8_decode(float *out, const float *q, const uint32_t *key_cache, const ui
 
 size_t pa_q8_prefill_workspace_size(int64_t num_rows, int num_seqs, int num_heads, int num_kv_heads, int head_size,
                                     int block_size, int max_blocks_per_seq, int dtype) {
-    if (check_prefill_shape(num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq,
+    pa_q8::PrefillArgs a;
+    if (check_prefill_shape(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq,
                             dtype) != PA_Q8_OK)
         return 0;
-    int sms = 0;
-    if (device_info(nullptr, &sms) != PA_Q8_OK) sms = 152;     // size query without a device
-    pa_q8::PrefillArgs a;
-    prefill_fill(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, dtype, sms);
     return pa_q8::prefill_workspace_bytes(a);
 }
 
@@ -559,7 +547,8 @@ int pa_q8_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64
                   const uint32_t *context_lens, const uint32_t *query_starts, int64_t num_rows, int num_seqs,
                   int num_heads, int num_kv_heads, int head_size, int block_size, int max_blocks_per_seq,
                   int64_t num_blocks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
-    int rc = check_prefill_shape(num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+    pa_q8::PrefillArgs a;
+    int rc = check_prefill_shape(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size,
                                  max_blocks_per_seq, dtype);
     if (rc != PA_Q8_OK) return rc;
     const int64_t row = (int64_t)num_heads * head_size;
@@ -573,11 +562,8 @@ int pa_q8_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64
         q_stride % vec)
         return PA_Q8_EALIGN;
     uint32_t *status = nullptr;
-    int sms = 0;
-    rc = device_info(&status, &sms);
+    rc = device_info(&status, nullptr);
     if (rc != PA_Q8_OK) return rc;
-    pa_q8::PrefillArgs a;
-    prefill_fill(a, num_rows, num_seqs, num_heads, num_kv_heads, head_size, block_size, max_blocks_per_seq, dtype, sms);
     const size_t need = pa_q8::prefill_workspace_bytes(a);
     if (!workspace || workspace_bytes < need) return PA_Q8_EWORKSPACE;
     if (!aligned16(workspace)) return PA_Q8_EALIGN;

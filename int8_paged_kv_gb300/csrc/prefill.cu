@@ -160,18 +160,17 @@ struct Params {
 // tiles; the way that should end first is taken.  (Two prompts of 512 rows behind
 // 130,000 and 60,000 tokens, 256 CTAs: 2634 us uncut, 1913 finely; 128 equal CTAs
 // of 8192 tokens: 196 us uncut, 270 finely.)
-constexpr int kWave = 152;             // SMs of a GB300: CTAs at a time
 constexpr int kMinPiece = 512;         // context tokens that pay for a piece of their own
 constexpr int kFine = 8;
 constexpr float kCost = 2.0f;          // 10,000 cycles
-constexpr int kMaySplit = 4 * kWave;   // CTAs without pieces above which nothing is cut
+constexpr int kMaySplit = 4;           // CTAs per SM, uncut, above which nothing is cut
 
 // Whether fine pieces can pay: ctas items of `longest` tiles at most, `share` tiles per SM,
 // the shorter half of them `low` long on average.
-__device__ inline bool fine_pays(float ctas, float longest, float share, float low, float min_piece) {
+__device__ inline bool fine_pays(float sms, float ctas, float longest, float share, float low, float min_piece) {
     const float fine = fmaxf(share / kFine, min_piece);
-    const float coarse = ctas <= kWave ? fminf(longest, share * (1.0f + ctas / kWave))
-                                       : fmaxf(fminf(longest, 1.5f * share), share + 0.5f * low);
+    const float coarse = ctas <= sms ? fminf(longest, share * (1.0f + ctas / sms))
+                                     : fmaxf(fminf(longest, 1.5f * share), share + 0.5f * low);
     return share * (1.0f + kCost / fine) + 0.5f * fine < coarse;
 }
 
@@ -284,7 +283,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
     };
     uint32_t piece = 0x7FFFFFFFu;
     const uint32_t ctas = items * P.g.groups;
-    if (P.may_split && ctas < kMaySplit) {
+    const uint32_t sms = a.num_sms;
+    if (P.may_split && ctas < kMaySplit * sms) {
         // each thread keeps to its items, so it may read what it wrote
         unsigned long long sum = 0;
         uint32_t top = 0;
@@ -314,9 +314,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(Params P) {
         }
         __syncthreads();
         const unsigned long long all = sum_tiles * P.g.groups;
-        const int waves = P.fine && fine_pays((float)ctas, (float)longest, (float)all / kWave,
-                                    (float)low_tiles / (float)max(low_items, 1u), (float)(kMinPiece / P.tn)) ? kFine : 1;
-        piece = max((uint32_t)(kMinPiece / P.tn), (uint32_t)((all + kWave * waves - 1) / (kWave * waves)));
+        const uint32_t ends = sms * (P.fine && fine_pays((float)sms, (float)ctas, (float)longest, (float)all / sms,
+                                                         (float)low_tiles / (float)max(low_items, 1u),
+                                                         (float)(kMinPiece / P.tn)) ? kFine : 1);
+        piece = max((uint32_t)(kMinPiece / P.tn), (uint32_t)((all + ends - 1) / ends));
     }
     uint32_t slots = 0, splits = 0;
     for (uint32_t i0 = 0; i0 < items; i0 += kPlanThreads) {
@@ -598,7 +599,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
 
     // the grid is the plan's upper bound
     const uint32_t entry = blockIdx.x / P.g.groups, cta = blockIdx.x % P.g.groups;
-    if (P.may_split && blockIdx.x >= kWave) {
+    if (P.may_split && blockIdx.x >= P.a.num_sms) {
         grid_dependency_wait();
         if (entry >= P.plan.head[0]) return;
     }
@@ -1394,15 +1395,15 @@ size_t layout(const PrefillArgs &a, Params &P) {
     Plan &p = P.plan;
     p.cap_items = most;
     // Whether fine pieces can pay at all (fine_pays, solved for the largest share that the room
-    // allows).  Where they cannot, no place is kept for them: every 152 CTAs that the grid has
-    // too many of cost 1 us.
-    const double ctas = (double)(most * g.groups), part = ctas / kWave, share = part * ((room + P.tn - 1) / P.tn);
-    P.fine = least * g.groups < kMaySplit && room >= 2 * kMinPiece &&
+    // allows).  Where they cannot, no place is kept for them: a CTA per SM that the grid has too
+    // many costs 1 us.
+    const double ctas = (double)(most * g.groups), part = ctas / a.num_sms, share = part * ((room + P.tn - 1) / P.tn);
+    P.fine = least * g.groups < kMaySplit * a.num_sms && room >= 2 * kMinPiece &&
              (part > 1.0 ? share > 36.0 : share * (part - 0.0625) > 16.0 || share * (part - 0.5) > 2.0);
-    P.may_split = P.fine || (least * g.groups < kWave && room >= 2 * kMinPiece);
-    const int64_t waves = P.fine ? kFine : 1;
+    P.may_split = P.fine || (least * g.groups < a.num_sms && room >= 2 * kMinPiece);
+    const int64_t ends = (int64_t)a.num_sms * (P.fine ? kFine : 1);
     // pieces of split items: tiles / piece of each, at most
-    p.cap_slots = P.may_split ? std::min<int64_t>(kWave * waves / g.groups + 1, most * ((room + P.tn) / kMinPiece)) : 0;
+    p.cap_slots = P.may_split ? std::min<int64_t>(ends / g.groups + 1, most * ((room + P.tn) / kMinPiece)) : 0;
     p.cap_entries = most + p.cap_slots;
     char *base = static_cast<char *>(a.workspace);
     size_t at = 0;
