@@ -93,3 +93,48 @@ def test_pieces_without_a_page(D, dtype):
     assert device_status() == pk.PA_Q8_DEV_BAD_BLOCK
     want, top = plain(c.q.float().cpu().numpy(), c.ok, c.ov, bt, c.w.context_lens, c.starts, c.w.scale, D, 16)
     check(got.float().cpu().numpy().astype(np.float64), want, top, dtype, units=f32_units(1, 1.9 * np.sqrt(D)))
+
+
+def widened(c, width):
+    """The case's tables, `width` pages wide; entries behind a sequence's pages name no page."""
+    from tests.gpu_helpers import dev_u32
+    bt = np.full((c.w.block_tables.shape[0], width), 0xFFFFFFFF, dtype=np.uint32)
+    bt[:, :c.w.block_tables.shape[1]] = c.w.block_tables
+    return dev_u32(bt)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_short_prompts_behind_wide_tables(D, dtype):
+    """Tables for 131,072 tokens: room for pieces in the plan, no context long enough for one, the same bits."""
+    import torch
+    from tests.gpu_helpers import device_status
+    lens = [64, 64, 1, 500, 0, 33, 64, 128]
+    c = Case(32, 8, D, 16, lens, [64, 64, 1, 64, 0, 33, 7, 100], dtype, seed=D)
+    narrow = c.run()
+    got = c.run(bt=widened(c, 8192))
+    assert torch.equal(got, narrow) and device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_long_and_short_contexts_behind_wide_tables(D, dtype):
+    """Pieces of the long one, the short ones whole."""
+    from tests.gpu_helpers import device_status
+    c = Case(8, 2, D, 16, [20000, 40, 700], [9, 40, 130], dtype, seed=D)
+    c.checked("wide", bt=widened(c, 65536))
+    assert device_status() == 0
+
+
+def test_size_of_a_wide_tables_plan(lib):  # noqa: F811
+    """What the header says: at most some 170 MB of records, 10 to 20 MB of sums."""
+    import ctypes
+    from int8_paged_kv_gb300 import _binding
+    for D in (64, 128, 256):
+        for dtype in (0, 1, 2):
+            for rows in (1, 8, 512, 4096, 32768):
+                for seqs in (1, 8, 64):
+                    n = _binding.lib().pa_q8_prefill_workspace_size(ctypes.c_int64(rows), seqs, 32, 8, D, 16, 1 << 16, dtype)
+                    assert 0 < n <= 190e6
