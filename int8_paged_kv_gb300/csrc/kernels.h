@@ -9,7 +9,7 @@
 namespace pa_q8 {
 
 // Bits of a pool's or a prompt call's status word, next to those of
-// device_util.cuh (PA_Q8_STATUS_* of the public header).
+// device_util.cuh (PA_Q8_DEV_* of the public header).
 constexpr uint32_t kDevBadSeq = 0x8u;
 constexpr uint32_t kDevNoBlock = 0x10u;
 constexpr uint32_t kDevBadRows = 0x20u;

@@ -158,7 +158,7 @@ struct Params {
 // items fill one wave; or finely, into pieces of about p / kFine, which even out
 // between the SMs however the items divide.  A piece costs the time of kCost
 // tiles; the way that should end first is taken.  (Two prompts of 512 rows behind
-// 130,000 and 60,000 tokens, 256 CTAs: 2634 us uncut, 1913 finely; 128 equal CTAs
+// 130,000 and 60,000 tokens, 256 CTAs: 2634 us uncut, 1695 finely; 128 equal CTAs
 // of 8192 tokens: 196 us uncut, 270 finely.)
 constexpr int kMinPiece = 512;         // context tokens that pay for a piece of their own
 constexpr int kFine = 8;
