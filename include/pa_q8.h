@@ -324,12 +324,13 @@ size_t pa_q8_decode_rows_workspace_size(int num_seqs, int num_rows, int num_head
  * token's weight times its V scale goes the same way, 2^-22 or 2^-11 of itself
  * off, but no finer than 2^-32 of the largest weight times the largest V scale
  * among any 64 tokens that the row has met: a token whose V is many powers of
- * two larger hides the others near it, even when its own weight is small.  The
- * accumulators lose, toward zero, about 1e-7 of what they hold per 16 tokens.
- * f32 rows, whose accumulators are emptied into f32 sums after every 1024
- * tokens, are off by that up to 1.2e-5 of the result at any length (2e-6 with V
- * around zero); 16-bit rows by up to 6e-9 per context token (8e-4 at 131072
- * tokens when the first ones have nearly all weight; 7e-5 with V around zero).
+ * two larger hides the others near it, even when its own weight is small; V
+ * scales below 2^-90 fade to zero.  The accumulators lose, toward zero, about
+ * 1e-7 of what they hold per 16 tokens.  f32 rows, whose accumulators are
+ * emptied into f32 sums after every 1024 tokens, are off by that up to 1.2e-5 of
+ * the result at any length (2e-6 with V around zero); 16-bit rows by up to 6e-9
+ * per context token (8e-4 at 131072 tokens when the first ones have nearly all
+ * weight; 7e-5 with V around zero).
  */
 int pa_q8_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64_t q_stride,
                   const uint32_t *key_cache, const uint32_t *value_cache,
