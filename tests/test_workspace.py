@@ -193,3 +193,23 @@ def test_two_streams_with_work_pending():
                 assert torch.equal(a, out), turn
                 out.fill_(float("nan"))
             torch.cuda.synchronize()
+
+
+@gpu
+def test_streams_by_object_and_by_handle():
+    """A stream of torch, its handle, the legacy default stream's two handles, a stream of another library's."""
+    import torch
+    from int8_paged_kv_gb300 import build
+    build.build()
+    from tests.test_prefill import Case
+    c = Case(8, 2, 128, 16, [3000, 50], [200, 50], "bfloat16", seed=30)
+    alone = c.run()
+    side = torch.cuda.Stream()
+    other = types.SimpleNamespace(cuda_stream=side.cuda_stream)
+    for stream in (side, side.cuda_stream, other, torch.cuda.ExternalStream(side.cuda_stream), 0, 1,
+                   torch.cuda.default_stream()):
+        out = torch.full_like(c.q, float("nan"))
+        torch.cuda.synchronize()
+        c.run(out=out, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, alone), stream
