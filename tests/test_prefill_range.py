@@ -38,8 +38,8 @@ def test_rows_past_32bit_offsets():
     q = torch.empty((70000, 65536), dtype=torch.float16, device="cuda")
     out = torch.empty_like(q)
     q[:, 1024:2048] = c.q.reshape(70000, 1024)
-    c.run(q=q[:, 1024:2048].unflatten(1, (8, 128)), out=out[:, 2048:].unflatten(1, (496, 128))[:, :8])
-    assert torch.equal(out[:, 2048:3072].reshape(-1), packed.reshape(-1))
+    c.run(q=q[:, 1024:2048].unflatten(1, (8, 128)), out=out[:, 4096:5120].unflatten(1, (8, 128)))
+    assert torch.equal(out[:, 4096:5120].reshape(-1), packed.reshape(-1))
 
 
 @gpu
