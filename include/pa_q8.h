@@ -394,9 +394,11 @@ size_t pa_q8_window_decode_workspace_size(int num_seqs, int num_heads, int num_k
  * pa_q8_window_prefill -- packed prompt rows: pa_q8_prefill under a window.  Row i
  * of the n_s rows of sequence s (query_starts) is at position c - (n_s - 1 - i) - 1;
  * a row before position 0 is written as zeros.  Every argument, status and flag, the
- * types, strides, the workspace's rules and the precision are those of pa_q8_prefill;
- * the accumulators of f32 rows are emptied after every 512 tokens (head size 256, up to
- * 768 tokens seen: not at all), which halves what they lose.
+ * types, strides, the workspace's rules and the precision of 16-bit rows are those of
+ * pa_q8_prefill.  f32 rows come out below 1e-6 of the result off (2-norm, normal values,
+ * any window): what an accumulator holds is added to f32 sums after every 384 tokens
+ * that it took.  At head size 256 one accumulator takes all tokens, at 64 and 128 two
+ * take 64 tokens in turn.  (So the workspace has their sums from windows of 384 tokens on.)
  */
 int pa_q8_window_prefill(void *out, const void *q, int dtype, int64_t out_stride, int64_t q_stride,
                          const uint32_t *key_cache, const uint32_t *value_cache,

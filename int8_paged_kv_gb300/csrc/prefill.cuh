@@ -70,11 +70,14 @@ enum Mode { kPair, kSplit, kSingle };
 // holds where all terms have one sign: 1.2e-5 at a flush when nearly all weight came
 // with the first job, a third of that when it came evenly.
 constexpr int kFlush = 16;
-// Under a window every 8 jobs: what a prompt loses at its last rows alone, a window of 1500 tokens loses at
-// every row (2-norm for normal values: 1.5e-6 of the result every 16 jobs, 0.9e-6 every 8; f32 sums in
-// order are 0.8e-6 off).  At head size 256, where one warpgroup flushes and the tensor cores wait for two
-// jobs' time, windows of up to 12 jobs keep one sum (under 700 tokens 1553 us, 1898 with a flush).
-constexpr int kWindowFlush = 8, kWindowOneSum = 12;
+// Under a window, which nearly every row has in full, every 6.  A sum of j jobs comes out j 1.3e-7 of the
+// result off beside the 3e-7 to 5e-7 of the other roundings (2-norm, normal values), and 6 is the most that keeps
+// all windows and head sizes below 1e-6: 0.90e-6, with 8 1.13e-6, with 12 1.54e-6 (f32 products and sums in
+// order 0.3e-6 to 1.1e-6).  A first flush takes a row tile about 15% longer, as the warpgroup that flushes moves all
+// columns while no weights are written; later ones less (8 prompts of up to 4096 rows, 6 for 8: 32 heads on 8,
+// head size 128, windows of 700, 800, 1024 and 1500: 528, 566, 676, 796 us -> 527, 665, 710, 806; 16 heads on 1,
+// head size 256, windows of 300, 500, 700 and 1500: 174, 204, 274, 375 us -> 174, 240, 277, 396).
+constexpr int kWindowFlush = 6;
 
 // 64 tokens a job leave room in TMEM for the weights beside the logits.
 constexpr int kTN = 64;
@@ -616,8 +619,6 @@ template <typename T, typename C, bool WIN>
 __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     constexpr int D = C::D, TN = C::TN, CT = C::CT, SUB = C::SUB, NP = C::NP, NS = C::NS, W = C::W;
     constexpr int FLUSH = NP == 1 ? 1 << 29 : WIN ? kWindowFlush : kFlush;    // 16-bit rows: never
-    // jobs of an accumulator that is not flushed
-    constexpr int ONE_SUM = WIN && NP == 2 && C::MODE == kSingle ? kWindowOneSum : FLUSH;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t s0 = smem_addr(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -676,9 +677,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
     const int steps = min(tiles * SUB, (seen_all + TN - 1) / TN - j0 * SUB);     // of TN tokens
     const int jobs = C::MODE == kPair ? 2 * steps : steps;
     // whether accumulator x is flushed before the end
-    auto flushes = [&](int x) { return NP == 2 && (C::MODE == kSingle ? jobs : (jobs - x + 1) / 2) > ONE_SUM; };
-    // whether job number x of accumulator `acc` begins a new sum
-    auto restarts = [&](int acc, int x) { return x % FLUSH == 0 && (x == 0 || ONE_SUM == FLUSH || flushes(acc)); };
+    auto flushes = [&](int x) { return NP == 2 && (C::MODE == kSingle ? jobs : (jobs - x + 1) / 2) > FLUSH; };
+    // whether job x begins a new sum of its accumulator
+    auto restarts = [](int x) { return (C::MODE == kSingle ? x : x >> 1) % FLUSH == 0; };
     if (flushes(0) && tid == 0) {
         // the SM's own place is free, unless its number is not below the count of SMs (CTAs that
         // all looked from place 0 on queued for it: a kernel that flushes took half again as long)
@@ -843,8 +844,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 tc_fence_after();
                 const uint64_t aV = dV + st * (C::KV_TILE / 16) + (step % SUB) * (TN * 128 / 16);
                 const uint32_t tP = tmem + C::TM_P + b * (NP * TN / 2);
-                const bool more = NP == 2 ? !restarts(C::MODE == kSingle ? 0 : b, C::MODE == kSingle ? job : job >> 1)
-                                          : job > (C::MODE == kSingle ? 0 : 1);
+                const bool more = NP == 2 ? !restarts(job) : job > (C::MODE == kSingle ? 0 : 1);
 #pragma unroll (NP == 2 ? 1 : NP)
                 for (int p = NP - 1; p >= 0; --p)
 #pragma unroll
@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                 l2.x *= f;
                 l2.y *= f;
                 const int before = C::MODE == kSingle ? job - 1 : job - 2;   // the accumulator's last PV
-                if (before >= 0 && (NP == 1 || !restarts(C::MODE == kSingle ? 0 : wg, C::MODE == kSingle ? job : job >> 1))) {     // (else PV starts it anew)
+                if (before >= 0 && (NP == 1 || !restarts(job))) {     // (else PV starts it anew)
                     ok = wait_for(pv_done(before & 1), (before >> 1) & 1, abort);
                     if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; return; }
                     tc_fence_after();
@@ -1223,8 +1223,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
                  wait_for(s_full(b), (job >> 1) & 1, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
-            if (NP == 2 && job >= (C::MODE == kSingle ? FLUSH : 2 * FLUSH) &&
-                restarts(C::MODE == kSingle ? 0 : wg, C::MODE == kSingle ? job : job >> 1)) {
+            if (NP == 2 && job >= (C::MODE == kSingle ? FLUSH : 2 * FLUSH) && restarts(job)) {
                 // the accumulator, added to the row's sums
                 const int before = C::MODE == kSingle ? job - 1 : job - 2;
                 ok = wait_for(pv_done(before & 1), (before >> 1) & 1, abort);
