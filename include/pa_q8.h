@@ -374,9 +374,12 @@ size_t pa_q8_prefill_workspace_size(int64_t num_rows, int num_seqs, int num_head
  *
  * Precision.  q and the weights go through the tensor cores as two f16 parts (22 bits),
  * sums are f32, and a 16-bit row is rounded once, when it is written.  f32 rows add up
- * 32 tokens at a time (2.5e-7 of the result, 2-norm, at any window; 3.5e-7 at head size
- * 256); 16-bit rows leave their sums to the tensor cores, which lose about 1e-7 of them
- * per 16 tokens of the piece of a window that one warp takes.
+ * 32 tokens at a time: about 2.5e-7 of the result off (2-norm, normal values; 4e-7 at head
+ * size 256) where a warp, or pair of warps, adds up few tokens, and where it adds up T of
+ * them the root of the squares of that and of 4e-9 sqrt(T), at most: 7e-7 at 32768, 1.4e-6
+ * at 131072.  A window is cut into pieces for warps unless there are as many sequences
+ * (times kv heads) as the GPU holds warps, some 600 to 1800.  16-bit rows leave their sums
+ * to the tensor cores, which lose about 1e-7 of them per 16 tokens of such a piece.
  */
 int pa_q8_window_decode(void *out, const void *q, int dtype, int64_t out_stride, int64_t q_stride,
                         const uint32_t *key_cache, const uint32_t *value_cache,
