@@ -56,40 +56,10 @@ namespace {
 // Warp (head tile ht, token slot ts) owns query heads h0 + 8 ht + (0..7) and
 // chunks ts, ts + SLOTS, ...; the HT warps of one token slot share its
 // chunk stream.  Fragment coordinates: gq = lane / 4, cq = lane % 4.
-//
-// K dimension of S = Q K^T: k-step ks uses, for lane column cq, code word
-// kword(cq, ks) of a token row -- 4 consecutive head dims in one u32.  The
-// A fragment (q) follows the same dimension order, so the sum is the plain
-// dot product.  Rows gq and gq + 8 of A are the hi and lo f16 parts of head
-// gq.
-//
-// N dimension of O = P V: the V words of four tokens at word vword(gq, jj)
-// give, byte lane e, the B fragments of n-tile 4 jj + e; output column n of
-// n-tile i is head dim 4 * vword(n, i / 4) + i % 4.  Both word maps visit
-// every word once and make a warp's shared-memory reads hit 32 distinct
-// banks when the token row stride (head_size/4 + 1 words) is 1 mod 32
-// (head sizes 128 and 256).
-template <int D>
-__device__ __forceinline__ int kword(int cq, int ks) {
-    if constexpr (D == 64) return 4 * cq + ks;
-    else return 8 * cq + (ks & 7) + 32 * (ks >> 3);
-}
-
-template <int D>
-__device__ __forceinline__ int vword(int n, int jj) {
-    if constexpr (D == 64) return 4 * (n & 3) + (n >> 2) + 2 * jj;
-    else return 8 * (n & 3) + (n >> 2) + 2 * (jj & 3) + 32 * (jj >> 2);
-}
+// The word maps of the fragments are in decode_common.cuh.
 
 // Head size 256: the q fragments of every head tile ([HT][D/16][32] uint4),
 // then each head's logit factor ([HT * 8] f32).
-// Head dims (in float4 units) held at float4 slot t of a per-warp record:
-// the slot order of the record store above.
-template <int D>
-__device__ __forceinline__ int tc_record_dim4(int t) {
-    return vword<D>(2 * (t & 3) + ((t >> 2) & 1), t >> 3);
-}
-
 template <int D, int HT>
 __host__ __device__ constexpr uint32_t tc_extra_bytes() {
     return D == 256 ? (uint32_t)HT * (D / 16) * 32 * 16 + (uint32_t)HT * 8 * 4 : 0u;

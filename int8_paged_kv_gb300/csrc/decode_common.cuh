@@ -239,6 +239,42 @@ __device__ void write_zero_rows(const Params &P, const Work &w) {
 
 __host__ __device__ constexpr uint32_t align_up(uint32_t x, uint32_t a) { return (x + a - 1) / a * a; }
 
+// ------------------------------------------------ mma.sync fragment order
+//
+// Of the tensor-core tiles (decode.cu, window_decode.cu), in fragment
+// coordinates gq = lane / 4, cq = lane % 4.
+//
+// K dimension of S = Q K^T: k-step ks uses, for lane column cq, code word
+// kword(cq, ks) of a token row -- 4 consecutive head dims in one u32.  The
+// A fragment (q) follows the same dimension order, so the sum is the plain
+// dot product.  Rows gq and gq + 8 of A are the hi and lo f16 parts of head
+// gq.
+//
+// N dimension of O = P V: the V words of four tokens at word vword(gq, jj)
+// give, byte lane e, the B fragments of n-tile 4 jj + e; output column n of
+// n-tile i is head dim 4 * vword(n, i / 4) + i % 4.  Both word maps visit
+// every word once and make a warp's shared-memory reads hit 32 distinct
+// banks when the token row stride (head_size/4 + 1 words) is 1 mod 32
+// (head sizes 128 and 256).
+template <int D>
+__device__ __forceinline__ int kword(int cq, int ks) {
+    if constexpr (D == 64) return 4 * cq + ks;
+    else return 8 * cq + (ks & 7) + 32 * (ks >> 3);
+}
+
+template <int D>
+__device__ __forceinline__ int vword(int n, int jj) {
+    if constexpr (D == 64) return 4 * (n & 3) + (n >> 2) + 2 * jj;
+    else return 8 * (n & 3) + (n >> 2) + 2 * (jj & 3) + 32 * (jj >> 2);
+}
+
+// Head dims (in float4 units) held at float4 slot t of a per-warp record:
+// float4 slot (2 jj + e) * 4 + cq holds those of column n = 2 cq + e of word group jj.
+template <int D>
+__device__ __forceinline__ int tc_record_dim4(int t) {
+    return vword<D>(2 * (t & 3) + ((t >> 2) & 1), t >> 3);
+}
+
 // Bytes of the CTA merge's scratch (merge_and_store): per-slot (m, l, E)
 // and accumulators of every head, then the per-head factors.  The kernels
 // carve it out of their chunk ring once the streams are drained, so it must

@@ -35,30 +35,6 @@ namespace {
 
 constexpr int kStreams = 4;               // of a CTA
 
-// Fragment coordinates of a warp's tile: gq = lane / 4, cq = lane % 4, and the code words
-// that meet there, as in the decode kernels: k-step ks of Q K^T has word kword(cq, ks) of a
-// token; output column n of n-tile i of P V is head dim 4 vword(n, i / 4) + i % 4.  Both maps
-// visit every word once and make a warp's shared-memory reads hit 32 banks at a row
-// of head_size / 4 + 1 words (head sizes 128 and 256).
-template <int D>
-__device__ __forceinline__ int kword(int cq, int ks) {
-    if constexpr (D == 64) return 4 * cq + ks;
-    else return 8 * cq + (ks & 7) + 32 * (ks >> 3);
-}
-
-template <int D>
-__device__ __forceinline__ int vword(int n, int jj) {
-    if constexpr (D == 64) return 4 * (n & 3) + (n >> 2) + 2 * jj;
-    else return 8 * (n & 3) + (n >> 2) + 2 * (jj & 3) + 32 * (jj >> 2);
-}
-
-// Head dims, in fours, of float4 slot t of a record: slot (2 jj + e) 4 + cq holds those
-// of column n = 2 cq + e of word group jj.
-template <int D>
-__device__ __forceinline__ int record_dim4(int t) {
-    return vword<D>(2 * (t & 3) + ((t >> 2) & 1), t >> 3);
-}
-
 struct WindowParams {
     PrefillArgs a;
     int log2B, log2ptok;
@@ -825,7 +801,7 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(WindowParams 
     const int64_t row = (int64_t)j.x * a.out_stride + ((int64_t)g * P.group + h0 + h) * D;
 #pragma unroll
     for (int x = 0; x < N4; ++x)
-        store_out4(a.out, row + 4 * record_dim4<D>(lane + 32 * x), a.dtype,
+        store_out4(a.out, row + 4 * tc_record_dim4<D>(lane + 32 * x), a.dtype,
                    make_float4(o[x].x * inv, o[x].y * inv, o[x].z * inv, o[x].w * inv));
 }
 
