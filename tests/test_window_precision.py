@@ -118,3 +118,27 @@ def test_single_tokens(H, D, warps, tokens, mean):
     logits = math.sqrt(2 * (D / 16 * 9.0e-8 ** 2 + 1.5e-7 ** 2))
     bound = math.hypot(logits, 4e-9 * math.sqrt(tokens))
     assert off(got[at], q[at], kc, vc, torch.full_like(at, tokens - 1), tokens, tokens, 0) <= bound
+
+
+@gpu
+@pytest.mark.parametrize("window", [368, 376, 379, 380, 384, 385, 760, 768, 769])
+@pytest.mark.parametrize("H,Hk,D", [(16, 1, 256), (8, 2, 128), (8, 2, 64)])
+def test_prompts_where_the_first_sums_begin(H, Hk, D, window):
+    """Windows at which the workspace gets room for sums and accumulators are first emptied into them; what
+    stands behind a workspace of the size asked for stays."""
+    import torch
+    import int8_paged_kv_gb300 as pk
+    rows, tokens = 200, 1000
+    gen = torch.Generator(device="cuda").manual_seed(D + window)
+    pages = -(-tokens // BLOCK)
+    kc, vc = quantised(gen, Hk, pages, D, 0.0), quantised(gen, Hk, pages, D, 0.0)
+    q = torch.randn((rows, H, D), device="cuda", generator=gen)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    need = pk.pa_q8_window_prefill_workspace_size(rows, 1, H, Hk, D, BLOCK, pages, window, 0, q.dtype)
+    memory = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device="cuda")
+    got = pk.pa_q8_window_prefill(torch.empty_like(q), q, kc, vc, torch.arange(pages, **i32)[None].contiguous(),
+                                  torch.tensor([tokens], **i32), torch.tensor([0, rows], **i32), num_kv_heads=Hk,
+                                  block_size=BLOCK, window=window, scale=D ** -0.5, workspace=memory[:need])
+    at = torch.arange(rows, device="cuda")
+    assert off(got, q, kc, vc, tokens - rows + at, tokens, window, 0) <= 1e-6
+    assert bool((memory[need:] == 0xA5).all())
