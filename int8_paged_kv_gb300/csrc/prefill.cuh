@@ -76,7 +76,8 @@ constexpr int kFlush = 16;
 // order 0.3e-6 to 1.1e-6).  A first flush takes a row tile about 15% longer, as the warpgroup that flushes moves all
 // columns while no weights are written; later ones less (8 prompts of up to 4096 rows, 6 for 8: 32 heads on 8,
 // head size 128, windows of 700, 800, 1024 and 1500: 528, 566, 676, 796 us -> 527, 665, 710, 806; 16 heads on 1,
-// head size 256, windows of 300, 500, 700 and 1500: 174, 204, 274, 375 us -> 174, 240, 277, 396).
+// head size 256, windows of 300, 500, 700 and 1500: 174, 204, 274, 375 us -> 174, 240, 277, 396; without a flush
+// 240 under 700).
 constexpr int kWindowFlush = 6;
 
 // 64 tokens a job leave room in TMEM for the weights beside the logits.
@@ -1193,8 +1194,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) prefill_kernel(Params P) {
             }
         };
         // A job of which this warp's rows see nothing: weights of zero, and nothing else moves.  (The
-        // two row tiles of a pair see different ones: bf16 under 256 tokens 298 -> 292 us.  Where there is one
-        // tile, few jobs are like that: head size 256, f32, 1.5% slower.)
+        // two row tiles of a pair see different ones: bf16, 17,762 rows, 32 heads on 8, under 256 tokens 245 -> 241 us,
+        // under 1024 381 -> 372.  Where there is one tile, few jobs are like that: head size 256, f32, 1.5% slower.)
         constexpr bool ZEROS = WIN && C::MODE == kPair;
         [[maybe_unused]] const int sees_max = ZEROS ? (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)max(0, sees)) : 0;
         [[maybe_unused]] const int from_min = ZEROS ? (int)__reduce_min_sync(0xFFFFFFFFu, (unsigned)from) : 0;
