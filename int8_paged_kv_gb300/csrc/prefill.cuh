@@ -73,8 +73,8 @@ constexpr int kFlush = 16;
 // Under a window, which nearly every row has in full, every 6.  A sum of j jobs comes out j 1.3e-7 of the
 // result off beside the 3e-7 to 5e-7 of the other roundings (2-norm, normal values), and 6 is the most that keeps
 // all windows and head sizes below 1e-6: 0.90e-6, with 7 1.00e-6, with 8 1.13e-6, with 12 1.54e-6 (f32 products
-// and sums in order 0.3e-6 to 1.1e-6).  A first flush takes a row tile about 15% longer, as the warpgroup that flushes moves all
-// columns while no weights are written; later ones less (8 prompts of up to 4096 rows, 6 for 8: 32 heads on 8,
+// and sums in order 0.3e-6 to 1.1e-6).  A first flush takes a call 15% to 25% longer, as the warpgroup that flushes
+// moves all columns while no weights are written; later ones less (8 prompts of up to 4096 rows, 6 for 8: 32 heads on 8,
 // head size 128, windows of 700, 800, 1024 and 1500: 528, 566, 676, 796 us -> 527, 665, 710, 806; 16 heads on 1,
 // head size 256, windows of 300, 500, 700 and 1500: 174, 204, 274, 375 us -> 174, 240, 277, 396; without a flush
 // 240 under 700).
